@@ -10,7 +10,13 @@ from .gdn import (GDNError, BwdArgs, FwdArgs, GatedDeltaRule, abi_version,  # no
                   debug_chunk_T, device_check,
                   gated_delta_rule, last_error, lib, make_args, make_bwd_args, select_kernel, select_segments,
                   status_string, workspace_bytes, workspace_for)
+from .layer import (Int8MatmulArgs, RecurrentArgs, RowsArgs, add_rms_norm_int8, call_int8_matmul,  # noqa: F401
+                    call_recurrent, call_rows, gated_rms_norm_int8, int8_matmul, int8_matmul_workspace_bytes,
+                    quantize_int8, recurrent_fwd)
 
-__all__ = ["chunk_fwd", "chunk_bwd", "gated_delta_rule", "GatedDeltaRule", "BwdArgs",
+__all__ = ["recurrent_fwd", "add_rms_norm_int8", "gated_rms_norm_int8", "quantize_int8", "int8_matmul",
+           "RecurrentArgs", "RowsArgs", "Int8MatmulArgs", "call_recurrent", "call_rows", "call_int8_matmul",
+           "int8_matmul_workspace_bytes",
+           "chunk_fwd", "chunk_bwd", "gated_delta_rule", "GatedDeltaRule", "BwdArgs",
            "make_bwd_args", "call_bwd", "bwd_workspace_bytes", "device_check", "workspace_bytes", "workspace_for", "GDNError", "FwdArgs", "make_args", "call", "select_kernel", "select_segments",
            "abi_version", "last_error", "status_string", "lib", "debug_chunk_T", "clear_workspace_cache"]

@@ -7,6 +7,7 @@
 
 #include "gdn_bwd.cuh"
 #include "gdn_internal.cuh"
+#include "gdn_serve.cuh"
 
 // Fixed scratch of gdn_chunk_fwd_static_scratch: the per-chunk T matrices of
 // the tensor-core path (24 KiB per chunk-head), GDN_STATIC_SCRATCH_BYTES in all.
@@ -16,12 +17,17 @@ namespace {
 
 thread_local char g_msg[512] = "";
 
+gdn_status vfail(gdn_status s, const char *fmt, va_list ap) {
+    vsnprintf(g_msg, sizeof(g_msg), fmt, ap);
+    if (getenv("GDN_LOG")) fprintf(stderr, "[gdn] %s: %s\n", gdn_status_string(s), g_msg);
+    return s;
+}
+
 gdn_status fail(gdn_status s, const char *fmt, ...) {
     va_list ap;
     va_start(ap, fmt);
-    vsnprintf(g_msg, sizeof(g_msg), fmt, ap);
+    vfail(s, fmt, ap);
     va_end(ap);
-    if (getenv("GDN_LOG")) fprintf(stderr, "[gdn] %s: %s\n", gdn_status_string(s), g_msg);
     return s;
 }
 
@@ -257,6 +263,23 @@ gdn_status resolve_bwd(const gdn_bwd_args *a, gdn::BwdParams *out) {
 
 }  // namespace
 
+namespace gdn {
+
+gdn_status api_fail(gdn_status s, const char *fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vfail(s, fmt, ap);
+    va_end(ap);
+    return s;
+}
+
+gdn_status api_ok() {
+    g_msg[0] = 0;
+    return GDN_OK;
+}
+
+}  // namespace gdn
+
 extern "C" {
 
 const char *gdn_status_string(gdn_status s) {
@@ -311,7 +334,14 @@ gdn_status gdn_device_check(void *stream) {
     const unsigned int fcode = gdn::fused_read_and_clear_error(&e);
     if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "device check: %s", cudaGetErrorString(e));
     if (code) return fail(GDN_ERR_DEVICE_CHECK, "split tensor-core kernel wait %u gave up", code);
+    const unsigned int pcode = gdn::pool_read_and_clear_error(&e);
+    if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "device check: %s", cudaGetErrorString(e));
+    const unsigned int mcode = gdn::int8_matmul_read_and_clear_error(&e);
+    if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "device check: %s", cudaGetErrorString(e));
     if (fcode) return fail(GDN_ERR_DEVICE_CHECK, "fused tensor-core kernel wait %u gave up", fcode);
+    if (pcode)
+        return fail(GDN_ERR_DEVICE_CHECK, "recurrent_fwd: slot or cu_seqlens of sequence %u out of bounds", pcode - 1);
+    if (mcode) return fail(GDN_ERR_DEVICE_CHECK, "int8 product kernel wait %u gave up", mcode);
     g_msg[0] = 0;
     return GDN_OK;
 }

@@ -33,7 +33,8 @@ MODES = {"exact": GDN_INV_EXACT, "neumann": GDN_INV_NEUMANN, "residual": GDN_INV
 
 EXPORTS = ("gdn_chunk_fwd", "gdn_select_kernel", "gdn_workspace_bytes", "gdn_device_check",
            "gdn_status_string", "gdn_last_error", "gdn_abi_version", "gdn_chunk_fwd_static_scratch",
-           "gdn_chunk_bwd", "gdn_bwd_workspace_bytes", "gdn_debug_chunk_T", "gdn_select_segments")
+           "gdn_chunk_bwd", "gdn_bwd_workspace_bytes", "gdn_debug_chunk_T", "gdn_select_segments",
+           "gdn_recurrent_fwd", "gdn_rows_int8", "gdn_int8_matmul", "gdn_int8_matmul_workspace_bytes")
 STATIC_SCRATCH_BYTES = 24 << 20   # GDN_STATIC_SCRATCH_BYTES
 
 
@@ -88,6 +89,8 @@ _lib = None
 def lib() -> ctypes.CDLL:
     """Load libgdn.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -119,6 +122,11 @@ def lib() -> ctypes.CDLL:
             L.gdn_debug_chunk_T.argtypes = [ctypes.POINTER(FwdArgs), ctypes.c_int32, ctypes.c_int32,
                                             ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p]
             L.gdn_debug_chunk_T.restype = ctypes.c_int
+            for name in ("gdn_recurrent_fwd", "gdn_rows_int8", "gdn_int8_matmul"):   # packed structs (layer.py)
+                getattr(L, name).argtypes = [ctypes.c_char_p, ctypes.c_void_p]
+                getattr(L, name).restype = ctypes.c_int
+            L.gdn_int8_matmul_workspace_bytes.argtypes = [ctypes.c_char_p]
+            L.gdn_int8_matmul_workspace_bytes.restype = ctypes.c_uint64
             _lib = L
     return _lib
 

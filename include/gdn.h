@@ -367,6 +367,130 @@ GDN_API uint64_t gdn_bwd_workspace_bytes(const gdn_bwd_args *args);
  * ordered on one stream are safe. */
 GDN_API gdn_status gdn_chunk_fwd_static_scratch(const gdn_fwd_args *args, void *stream);
 
+/* ------------------------------------------------------ decode-layer operators
+ *
+ * What a quantised Gated DeltaNet layer runs around and in place of the
+ * chunkwise pass when it serves ("Quando o 'Bom o Suficiente' e Otimo:
+ * Aproximacao de Inversao de Matriz Baseada Apenas em Multiplicacao para Gated
+ * DeltaNet Quantizado" is about that layer; the pages print none of these
+ * steps):
+ *
+ *   hidden -> gdn_add_rms_norm_int8 -> gdn_int8_matmul (q, k, v, gate, ...)
+ *          -> gdn_recurrent_fwd -> gdn_gated_rms_norm_int8 -> gdn_int8_matmul
+ *
+ * Rows in 8 bits.  A row y of numbers is held as int8 steps and one fp32
+ * scale: scale = max|y| / 127, step = y / scale rounded to nearest (ties to
+ * even), in [-127, 127].  A row whose scale would be below 2^-126 is held as
+ * scale 0 and steps 0; a row with an infinity or a NaN as scale NaN and steps
+ * 0, so that every product with it is NaN.
+ *
+ * Ownership and errors as gdn_chunk_fwd: caller-allocated device buffers,
+ * arguments checked on the host before any launch, asynchronous on `stream`.
+ * Calls with no rows (or sequences) return GDN_OK and launch nothing.  Strides
+ * are in elements.  None of the calls keeps state or allocates.  They may be
+ * captured into CUDA graphs. */
+
+/* Gated delta rule, token by token, on a pool of states:
+ *
+ *   S_t = S_{t-1} alpha_t (I - beta_t k_t k_t^T) + beta_t v_t k_t^T,  o_t = S_t q_t
+ *
+ * for `seqs` sequences of any lengths, packed one after another along the
+ * token rows.  Sequence s owns rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1 and
+ * the state at index slots[s] of the pool, which it reads and then overwrites.
+ * Value head h reads key head h / (H / Hk).
+ *
+ * - A sequence of no tokens leaves its state as it was.  slots[s] = -1 marks an
+ *   entry that holds no sequence: its rows of o become 0, no state is touched.
+ * - Rows of o that belong to no sequence (before cu_seqlens[0], behind
+ *   cu_seqlens[seqs]) are left as they were.
+ * - A slot may be named by one sequence of a call only: two that name the same
+ *   slot race on its state.
+ * - cu_seqlens and slots are read on the device.  An entry outside the pool
+ *   (other than -1), or a range that is decreasing or outside the rows, is
+ *   recorded for gdn_device_check; such an entry counts as slot -1, such a
+ *   range as empty.
+ * - With qk_norm, q_t and k_t are first divided by sqrt(sum of squares + qk_eps).
+ *
+ * The state and all sums are fp32.  q, k, v may be parts of a wider row. */
+typedef struct {
+    int32_t rows, seqs;         /* token rows of q, k, v, alpha, beta, o; sequences (>= 0) */
+    int32_t H, Hk;              /* value heads; key heads (H a multiple of Hk) */
+    int32_t dk, dv;             /* dk: 16, 32, 64 or 128; dv: 32, 64, 96 or 128 */
+    int32_t pool;               /* states in the pool (>= 1) */
+    int32_t io_dtype, o_dtype;  /* gdn_dtype of q, k, v; of o */
+    int32_t qk_norm;            /* 0: q, k as given; 1: normalised here */
+    float qk_eps;               /* >= 0 */
+    const void *q, *k, *v;      /* [rows][Hk][dk], [rows][Hk][dk], [rows][H][dv] */
+    int64_t q_row, q_head, k_row, k_head, v_row, v_head;   /* strides (>= 0) */
+    const float *alpha, *beta;  /* [rows][H] (heads adjacent), or NULL (=> 1) */
+    int64_t alpha_row, beta_row;
+    const int32_t *cu_seqlens;  /* [seqs + 1], or NULL: one token a sequence (rows == seqs) */
+    const int32_t *slots;       /* [seqs], or NULL: sequence s owns state s (pool >= seqs) */
+    float *state;               /* [pool][H][dk][dv] (h = S^T), 16-byte aligned, in place */
+    void *o;                    /* [rows][H][dv] */
+} gdn_recurrent_args;
+
+GDN_API gdn_status gdn_recurrent_fwd(const gdn_recurrent_args *args, void *stream);
+
+/* Rows in 8 bits, plain or after a norm.  One call serves three operators:
+ *
+ *   GDN_ROWS_PLAIN  y = x
+ *   GDN_ROWS_NORM   h = x + residual,  y = h / sqrt(mean(h^2) + eps) * weight;
+ *                   residual_out = h rounded to the residual's type
+ *   GDN_ROWS_GATED  for each head of `head` channels: y = x / sqrt(mean(x^2) + eps)
+ *                   * weight * gate / (1 + e^-gate); the scale is the whole row's
+ *
+ * Sums of squares are fp32.  residual_out may be residual itself, or x itself
+ * when the types and the strides agree; no other output may overlap an input. */
+typedef enum { GDN_ROWS_PLAIN = 0, GDN_ROWS_NORM = 1, GDN_ROWS_GATED = 2 } gdn_rows_op;
+
+typedef struct {
+    int32_t op;                 /* gdn_rows_op */
+    int32_t rows, width;        /* rows >= 0; 1 <= width <= 32768 */
+    int32_t head;               /* GATED: channels a head, a multiple of 8 up to 256 that divides width */
+    int32_t x_dtype, residual_dtype, weight_dtype;   /* gdn_dtype; gate has x's */
+    float eps;                  /* > 0 (NORM, GATED) */
+    const void *x;              /* [rows][width] */
+    const void *residual;       /* NORM: [rows][width] or NULL (=> 0) */
+    const void *gate;           /* GATED: [rows][width] */
+    const void *weight;         /* NORM: [width] or NULL (=> 1); GATED: [head] or NULL (=> 1) */
+    int64_t x_row, residual_row, gate_row, residual_out_row, q_row;
+    void *residual_out;         /* NORM with a residual: [rows][width], required then */
+    int8_t *q;                  /* [rows][width] steps */
+    float *scale;               /* [rows] */
+} gdn_rows_args;
+
+GDN_API gdn_status gdn_rows_int8(const gdn_rows_args *args, void *stream);
+
+/* Product of rows in 8 bits:
+ *
+ *   out[m][n] = x_scale[m] w_scale[n] sum_k x[m][k] w[n][k] + bias[n]
+ *
+ * The sum is exact (32-bit integers; 2^14 K < 2^31 bounds K).  The tensor
+ * memory accelerator wants rows that start on 16 bytes: where x or w has
+ * another base or stride, a kernel first copies it to such rows in the
+ * workspace, which costs one more pass over it each call. */
+typedef struct {
+    int32_t M, N, K;            /* M >= 0, N >= 1, 1 <= K <= 131071 */
+    int32_t out_dtype;          /* gdn_dtype */
+    const int8_t *x;            /* [M][K] */
+    const int8_t *w;            /* [N][K] */
+    int64_t x_row, w_row, out_row;
+    const float *x_scale;       /* [M] */
+    const float *w_scale;       /* [N] */
+    const float *bias;          /* [N] or NULL (=> 0) */
+    void *out;                  /* [M][N] */
+    void *workspace;            /* >= gdn_int8_matmul_workspace_bytes(args) bytes, 16-byte aligned */
+    uint64_t workspace_bytes;
+} gdn_int8_matmul_args;
+
+GDN_API gdn_status gdn_int8_matmul(const gdn_int8_matmul_args *args, void *stream);
+
+/* Workspace of gdn_int8_matmul: 0 when x and w start on 16 bytes and their row
+ * strides are multiples of 16, else the copies' size; 0 with gdn_last_error()
+ * set if the arguments are invalid.  Host only. */
+GDN_API uint64_t gdn_int8_matmul_workspace_bytes(const gdn_int8_matmul_args *args);
+
 #ifdef __cplusplus
 }
 #endif
