@@ -1,31 +1,21 @@
-// Gated delta rule, token by token, for a ragged batch on a pool of states
-// (h = S^T, d_k x d_v, fp32):
+// Gated delta rule, token by token, on a pool of states (h = S^T, d_k x d_v, fp32):
 //
 //   p   = h^T k_t                          (= S_{t-1} k_t)
 //   u   = beta_t (v_t - alpha_t p)
 //   h  <- alpha_t h + k_t u^T
 //   o_t = h^T q_t
 //
-// Columns of h never meet: a warp takes 16 of them through all tokens of one
-// sequence and head, with its 16 columns of h in registers and no barrier.
-// Lane = row group (8) x column quad (4): R = d_k / 8 rows by 4 columns a lane,
-// so a row's 16 columns are 64 contiguous bytes of the state.  The two sums over
-// d_k go by halving exchanges: 4 shuffles leave each lane one column's sum, in
-// which it forms that column's u, and 3 more hand the 4 columns' u round.
-//
-// A step of one token is bound by reading and writing the states (8 d_k d_v
-// bytes a head); a long sequence by the chain p -> u -> h of each token, beside
-// which the next token's q, k, v and gates are already on their way.
+// Two kernels: one token a sequence (step), and ragged sequences.
 #include <cuda_bf16.h>
+
+#include <type_traits>
 
 #include "gdn_serve.cuh"
 
 namespace gdn {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kCols = 16;       // value columns a warp
-constexpr int kGroups = 8;      // row groups a warp
+constexpr int kGroups = 8;      // threads that share a column's d_k rows
 
 // Sequence whose cu_seqlens range or slot is out of bounds: 1 + its index.
 __device__ unsigned int g_pool_error = 0;
@@ -35,181 +25,548 @@ __device__ __forceinline__ float load1(const void *p, int64_t i, bool bf16) {
     return reinterpret_cast<const float *>(p)[i];
 }
 
-// R consecutive numbers as they lie in memory, so that a token's q and k wait
-// in as few registers as they have bytes.
-template <int R, bool BF16>
+// N consecutive numbers as they lie in memory, so that they wait in as few registers
+// as they have bytes, and nothing waits for them before they are used.
+template <int N, bool BF16>
 struct Raw {
-    static constexpr int kWords = BF16 ? (R + 1) / 2 : R;
+    static constexpr int kWords = BF16 ? (N + 1) / 2 : N;
     uint32_t w[kWords];
 
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int j = 0; j < kWords; ++j) w[j] = 0;
+    }
+    // VEC: base + i lies on N numbers' bytes, or on 16
     template <bool VEC>
     __device__ __forceinline__ void load(const void *base, int64_t i) {
-        if constexpr (VEC && kWords % 4 == 0) {
-            const uint4 *s = reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(base) + i * (BF16 ? 2 : 4));
+        const char *from = reinterpret_cast<const char *>(base) + i * (BF16 ? 2 : 4);
+        if constexpr (BF16 && N == 1) {
+            w[0] = __ldg(reinterpret_cast<const uint16_t *>(from));
+        } else if constexpr (VEC && kWords % 4 == 0) {
 #pragma unroll
             for (int j = 0; j < kWords / 4; ++j) {
-                const uint4 x = __ldg(s + j);
+                const uint4 x = __ldg(reinterpret_cast<const uint4 *>(from) + j);
                 w[4 * j] = x.x; w[4 * j + 1] = x.y; w[4 * j + 2] = x.z; w[4 * j + 3] = x.w;
             }
-        } else if constexpr (BF16) {
-            const uint16_t *s = reinterpret_cast<const uint16_t *>(base) + i;
+        } else if constexpr (VEC && kWords == 2) {
+            const uint2 x = __ldg(reinterpret_cast<const uint2 *>(from));
+            w[0] = x.x; w[1] = x.y;
+        } else if constexpr (VEC || !BF16) {
 #pragma unroll
-            for (int j = 0; j < R / 2; ++j) w[j] = (uint32_t)__ldg(s + 2 * j) | ((uint32_t)__ldg(s + 2 * j + 1) << 16);
+            for (int j = 0; j < kWords; ++j) w[j] = __ldg(reinterpret_cast<const uint32_t *>(from) + j);
         } else {
-            const uint32_t *s = reinterpret_cast<const uint32_t *>(base) + i;
+            const uint16_t *x = reinterpret_cast<const uint16_t *>(from);
 #pragma unroll
-            for (int j = 0; j < R; ++j) w[j] = __ldg(s + j);
+            for (int j = 0; j < N / 2; ++j) w[j] = (uint32_t)__ldg(x + 2 * j) | ((uint32_t)__ldg(x + 2 * j + 1) << 16);
         }
     }
-
     __device__ __forceinline__ float get(int r) const {
         if constexpr (BF16) return __uint_as_float(r & 1 ? w[r / 2] & 0xffff0000u : w[r / 2] << 16);
         else return __uint_as_float(w[r]);
     }
 };
 
-__device__ __forceinline__ float xor_add(float x, int mask) { return x + __shfl_xor_sync(~0u, x, mask); }
-
-// Sums over the 8 row groups; lane gets the one of column `lane_col`.
-__device__ __forceinline__ float reduce_columns(const float (&x)[4], int lane) {
-    const bool hi = lane & 16, odd = lane & 8;
-    const float a = hi ? x[2] : x[0], b = hi ? x[3] : x[1];
-    const float c = a + __shfl_xor_sync(~0u, hi ? x[0] : x[2], 16);
-    const float d = b + __shfl_xor_sync(~0u, hi ? x[1] : x[3], 16);
-    const float e = (odd ? d : c) + __shfl_xor_sync(~0u, odd ? c : d, 8);
-    return xor_add(e, 4);
+__device__ __forceinline__ void store_o(const PoolParams &p, int64_t i, float x) {
+    if (p.o_bf16) reinterpret_cast<__nv_bfloat16 *>(p.o)[i] = __float2bfloat16_rn(x);
+    else reinterpret_cast<float *>(p.o)[i] = x;
 }
 
-template <int R, bool BF16, bool VEC>
-__global__ void __launch_bounds__(kWarps * 32) recurrent_pool_kernel(const PoolParams p) {
-    const int lane = threadIdx.x & 31;
-    const int slices = p.dv / kCols;
-    const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (item >= (int64_t)p.seqs * p.H * slices) return;
-    const int slice = (int)(item % slices);
-    const int h = (int)(item / slices % p.H);
-    const int s = (int)(item / slices / p.H);
-
-    int begin = s, end = s + 1;
+// The state of sequence s (-1: none), and its rows.  False where nothing is to be done.
+__device__ __forceinline__ bool sequence(const PoolParams &p, int s, int *slot, int *begin, int *end) {
+    *begin = s;
+    *end = s + 1;
     if (p.cu_seqlens) {
-        begin = p.cu_seqlens[s];
-        end = p.cu_seqlens[s + 1];
-        if (begin < 0 || end < begin || end > p.rows) {
-            if (lane == 0) atomicCAS(&g_pool_error, 0u, (unsigned)s + 1u);
-            return;
+        *begin = p.cu_seqlens[s];
+        *end = p.cu_seqlens[s + 1];
+        if (*begin < 0 || *end < *begin || *end > p.rows) {
+            if (threadIdx.x == 0) atomicCAS(&g_pool_error, 0u, (unsigned)s + 1u);
+            return false;
         }
     }
-    int slot = p.slots ? p.slots[s] : s;
-    if (slot < -1 || slot >= p.pool) {
-        if (lane == 0) atomicCAS(&g_pool_error, 0u, (unsigned)s + 1u);
-        slot = -1;
+    *slot = p.slots ? p.slots[s] : s;
+    if (*slot < -1 || *slot >= p.pool) {
+        if (threadIdx.x == 0) atomicCAS(&g_pool_error, 0u, (unsigned)s + 1u);
+        *slot = -1;
     }
-    if (begin == end) return;
-    if (slot < 0) {                      // no sequence: zero rows of o
-        for (int64_t t = begin + (lane >> 4); t < end; t += 2) {
-            const int64_t i = (t * p.H + h) * p.dv + slice * kCols + (lane & 15);
-            if (p.o_bf16) reinterpret_cast<__nv_bfloat16 *>(p.o)[i] = __float2bfloat16_rn(0.f);
-            else reinterpret_cast<float *>(p.o)[i] = 0.f;
-        }
+    return *begin < *end;
+}
+
+// One token a sequence.  Bound by reading and writing the states, 8 d_k d_v bytes
+// a head.  A block takes one sequence and head: thread = row group (8) x column
+// quad, R = d_k / 8 rows by 4 columns in registers, so that a warp reads whole rows
+// of the state.  With both sums over d_k taken from the old state,
+//
+//   o = h_new^T q = alpha (h^T q) + (k . q) u,
+//
+// they (and the squares of k and q, since both sums are linear in them) cross the
+// block in one exchange through shared memory.
+template <int R, bool BF16, bool VEC>
+__global__ void __launch_bounds__(256, 2) recurrent_step_kernel(const PoolParams p) {
+    __shared__ float4 sums[2][kGroups][32];
+    __shared__ float dots[3][kGroups];
+    const int quads = p.dv / 4;
+    const int group = threadIdx.x / quads, quad = threadIdx.x % quads;
+    const int s = blockIdx.x / p.H, h = blockIdx.x % p.H;
+    int slot, t, end;
+    if (!sequence(p, s, &slot, &t, &end)) return;
+    const int64_t oi = ((int64_t)t * p.H + h) * p.dv + quad * 4;
+    if (slot < 0) {                      // no sequence: a zero row of o
+        if (group == 0)
+            for (int c = 0; c < 4; ++c) store_o(p, oi + c, 0.f);
         return;
     }
-
-    const int group = lane >> 2, quad = lane & 3;
     const int row0 = group * R, hk = h / (p.H / p.Hk);
-    float4 *hp = reinterpret_cast<float4 *>(p.state + (((int64_t)slot * p.H + h) * p.dk + row0) * p.dv + slice * kCols) + quad;
-    const int pitch = p.dv / 4;          // float4 a row
-    float hr[R][4];
+    float4 *hp = reinterpret_cast<float4 *>(p.state + (((int64_t)slot * p.H + h) * p.dk + row0) * p.dv) + quad;
+    float4 x[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) x[r] = __ldcg(hp + r * quads);
+    Raw<R, BF16> k, q;
+    k.template load<VEC>(p.k, (int64_t)t * p.k_row + (int64_t)hk * p.k_head + row0);
+    q.template load<VEC>(p.q, (int64_t)t * p.q_row + (int64_t)hk * p.q_head + row0);
+    float v[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) v[c] = load1(p.v, (int64_t)t * p.v_row + (int64_t)h * p.v_head + quad * 4 + c, BF16);
+    const float a = p.alpha ? __ldg(p.alpha + (int64_t)t * p.alpha_row + h) : 1.f;
+    const float be = p.beta ? __ldg(p.beta + (int64_t)t * p.beta_row + h) : 1.f;
+
+    float4 hk4 = make_float4(0.f, 0.f, 0.f, 0.f), hq4 = hk4;
+    float kk = 0.f, qq = 0.f, kq = 0.f;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        const float4 x = __ldcg(hp + r * pitch);
-        hr[r][0] = x.x; hr[r][1] = x.y; hr[r][2] = x.z; hr[r][3] = x.w;
+        const float kr = k.get(r), qr = q.get(r);
+        hk4.x = fmaf(x[r].x, kr, hk4.x); hk4.y = fmaf(x[r].y, kr, hk4.y);
+        hk4.z = fmaf(x[r].z, kr, hk4.z); hk4.w = fmaf(x[r].w, kr, hk4.w);
+        hq4.x = fmaf(x[r].x, qr, hq4.x); hq4.y = fmaf(x[r].y, qr, hq4.y);
+        hq4.z = fmaf(x[r].z, qr, hq4.z); hq4.w = fmaf(x[r].w, qr, hq4.w);
+        kk = fmaf(kr, kr, kk); qq = fmaf(qr, qr, qq); kq = fmaf(kr, qr, kq);
     }
-
-    // the column whose sums this lane holds after reduce_columns
-    const int col = slice * kCols + quad * 4 + ((lane >> 4) & 1) * 2 + ((lane >> 3) & 1);
-    const int64_t qo = (int64_t)hk * p.q_head + row0, ko = (int64_t)hk * p.k_head + row0;
-    const int64_t vo = (int64_t)h * p.v_head + col;
-    Raw<R, BF16> kn, qn;
-    float vn, an, bn;
-    auto fetch = [&](int64_t t) {
-        kn.template load<VEC>(p.k, t * p.k_row + ko);
-        qn.template load<VEC>(p.q, t * p.q_row + qo);
-        vn = load1(p.v, t * p.v_row + vo, BF16);
-        an = p.alpha ? __ldg(p.alpha + t * p.alpha_row + h) : 1.f;
-        bn = p.beta ? __ldg(p.beta + t * p.beta_row + h) : 1.f;
+    sums[0][group][quad] = hk4;
+    sums[1][group][quad] = hq4;
+    if (quad == 0) { dots[0][group] = kk; dots[1][group] = qq; dots[2][group] = kq; }
+    __syncthreads();
+    kk = qq = kq = 0.f;
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) { kk += dots[0][g]; qq += dots[1][g]; kq += dots[2][g]; }
+    const float kn = p.qk_norm ? 1.f / sqrtf(kk + p.qk_eps) : 1.f, qn = p.qk_norm ? 1.f / sqrtf(qq + p.qk_eps) : 1.f;
+    auto total = [&](int i) {
+        float4 y = sums[i][0][quad];
+#pragma unroll
+        for (int g = 1; g < kGroups; ++g) {
+            const float4 z = sums[i][g][quad];
+            y.x += z.x; y.y += z.y; y.z += z.z; y.w += z.w;
+        }
+        return y;
     };
-    fetch(begin);
-    for (int64_t t = begin; t < end; ++t) {
-        float ks[R], qs[R];
+    const float4 w = total(0);
+    const float u[4] = {be * (v[0] - a * (kn * w.x)), be * (v[1] - a * (kn * w.y)), be * (v[2] - a * (kn * w.z)),
+                        be * (v[3] - a * (kn * w.w))};
 #pragma unroll
-        for (int r = 0; r < R; ++r) { ks[r] = kn.get(r); qs[r] = qn.get(r); }
-        const float v = vn, a = an, be = bn;
-        if (t + 1 < end) fetch(t + 1);
-        if (p.qk_norm) {
-            float kk = 0.f, qq = 0.f;
-#pragma unroll
-            for (int r = 0; r < R; ++r) { kk += ks[r] * ks[r]; qq += qs[r] * qs[r]; }
-#pragma unroll
-            for (int m = 4; m < 32; m *= 2) { kk = xor_add(kk, m); qq = xor_add(qq, m); }
-            kk = 1.f / sqrtf(kk + p.qk_eps);
-            qq = 1.f / sqrtf(qq + p.qk_eps);
-#pragma unroll
-            for (int r = 0; r < R; ++r) { ks[r] *= kk; qs[r] *= qq; }
-        }
-        float x[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) x[c] = fmaf(hr[r][c], ks[r], x[c]);
-        const float uc = be * (v - a * reduce_columns(x, lane));
-        // u of the quad's 4 columns: from the neighbours across bits 3 and 4
-        const float un = __shfl_xor_sync(~0u, uc, 8);
-        const bool hi = lane & 16, odd = lane & 8;
-        const float u0 = odd ? un : uc, u1 = odd ? uc : un;
-        const float w0 = __shfl_xor_sync(~0u, u0, 16), w1 = __shfl_xor_sync(~0u, u1, 16);
-        const float u[4] = {hi ? w0 : u0, hi ? w1 : u1, hi ? u0 : w0, hi ? u1 : w1};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) x[c] = 0.f;
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                hr[r][c] = fmaf(ks[r], u[c], a * hr[r][c]);
-                x[c] = fmaf(hr[r][c], qs[r], x[c]);
-            }
-        const float o = reduce_columns(x, lane);
-        if (!(lane & 4)) {
-            const int64_t i = (t * p.H + h) * p.dv + col;
-            if (p.o_bf16) reinterpret_cast<__nv_bfloat16 *>(p.o)[i] = __float2bfloat16_rn(o);
-            else reinterpret_cast<float *>(p.o)[i] = o;
-        }
+    for (int r = 0; r < R; ++r) {
+        const float kr = k.get(r) * kn;
+        __stcg(hp + r * quads, make_float4(fmaf(kr, u[0], a * x[r].x), fmaf(kr, u[1], a * x[r].y),
+                                           fmaf(kr, u[2], a * x[r].z), fmaf(kr, u[3], a * x[r].w)));
     }
-#pragma unroll
-    for (int r = 0; r < R; ++r) __stcg(hp + r * pitch, make_float4(hr[r][0], hr[r][1], hr[r][2], hr[r][3]));
+    if (group == 0) {
+        const float4 y = total(1);
+        const float b = kq * kn * qn, aq = a * qn;
+        store_o(p, oi, fmaf(b, u[0], aq * y.x));
+        store_o(p, oi + 1, fmaf(b, u[1], aq * y.y));
+        store_o(p, oi + 2, fmaf(b, u[2], aq * y.z));
+        store_o(p, oi + 3, fmaf(b, u[3], aq * y.w));
+    }
 }
 
-template <int R>
-void launch_r(const PoolParams &p, unsigned blocks, cudaStream_t stream) {
-    const int threads = kWarps * 32;
-    if (p.io_bf16) {
-        if (p.vec) recurrent_pool_kernel<R, true, true><<<blocks, threads, 0, stream>>>(p);
-        else recurrent_pool_kernel<R, true, false><<<blocks, threads, 0, stream>>>(p);
-    } else {
-        if (p.vec) recurrent_pool_kernel<R, false, true><<<blocks, threads, 0, stream>>>(p);
-        else recurrent_pool_kernel<R, false, false><<<blocks, threads, 0, stream>>>(p);
+// Two floats that one instruction works on (fma.rn.f32x2).
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 pack(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack(F2 x, float *lo, float *hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(*lo), "=f"(*hi) : "l"(x.v)); }
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ float both(F2 x) {
+    float lo, hi;
+    unpack(x, &lo, &hi);
+    return lo + hi;
+}
+
+__device__ __forceinline__ float xor_add(float x, int mask) { return x + __shfl_xor_sync(~0u, x, mask); }
+
+constexpr int kCols = 16;       // value columns a warp
+constexpr int kFour = 4;        // tokens a step of the ragged kernel takes at once
+
+// The sequence of rank `rank` when those with more tokens come first, to within the
+// power of two of their tokens: blocks start in order, and a long sequence that
+// starts last leaves the device to itself.  Each block counts for itself.
+template <int THREADS>
+__device__ __forceinline__ int longest_first(const PoolParams &p, int rank) {
+    __shared__ int count[33], found;
+    auto bucket = [&](int s) {           // 32: none, else leading zeros of the tokens
+        const int n = p.cu_seqlens[s + 1] - p.cu_seqlens[s];
+        return n > 0 ? __clz(n) : 32;
+    };
+    if (threadIdx.x < 33) count[threadIdx.x] = 0;
+    __syncthreads();
+    for (int s = threadIdx.x; s < p.seqs; s += THREADS) atomicAdd(&count[bucket(s)], 1);
+    __syncthreads();
+    int mine = 0;
+    for (; rank >= count[mine]; ++mine) rank -= count[mine];
+    // the rank-th of that bucket, in order
+    for (int first = 0; first < p.seqs; first += THREADS) {
+        const int s = first + threadIdx.x;
+        const bool is = s < p.seqs && bucket(s) == mine;
+        const unsigned votes = __ballot_sync(~0u, is);
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) count[threadIdx.x >> 5] = __popc(votes);
+        __syncthreads();
+        int before = __popc(votes & ((1u << (threadIdx.x & 31)) - 1)), all = 0;
+        for (int w = 0; w < THREADS / 32; ++w) {
+            if (w < (int)(threadIdx.x >> 5)) before += count[w];
+            all += count[w];
+        }
+        if (is && before == rank) found = s;
+        if (rank < all) break;
+        rank -= all;
     }
+    __syncthreads();
+    return found;
+}
+
+template <int N>
+__device__ __forceinline__ void store_few(float *p, const float (&x)[N]) {
+    if constexpr (N == 4) *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+    else if constexpr (N == 2) *reinterpret_cast<float2 *>(p) = make_float2(x[0], x[1]);
+    else p[0] = x[0];
+}
+
+// Ragged sequences.  Columns of h never meet: a block takes one sequence, head and
+// W * 16 columns, and each warp 16 of them through all tokens, with h in registers.
+// Lane = row group (8) x column quad (4), R = d_k / 8 rows by 4 columns, as pairs of
+// rows for the two-float fma.
+//
+// The chain p -> u -> h would cost a token two exchanges over d_k, one after the
+// other, so tokens go in fours, by forward substitution: with h = A g (A the product
+// of the decays), P_i = g^T k_i and Q_i = g^T q_i of the four from the old g, and the
+// dot products of the four's keys and queries,
+//
+//   u'_i = beta_i v_i / A_i - beta_i (P_i + sum_{j<i} (k_j . k_i) u'_j)
+//   o_i  = A_i (Q_i + sum_{j<=i} (k_j . q_i) u'_j),     g <- g + sum_i k_i u'_i,
+//
+// which is the same recurrence in fp32 and has one exchange for the four.  Bound by
+// its fma's, 3 for each of the d_k d_v cells of a token, two in an instruction.  A
+// goes into g before it leaves [2^-32, 2^32]; a decay that would take it past
+// [2^-64, 2^64] within four tokens ends the four early.
+//
+// The warps bring the tokens after next into shared memory, as fp32 and normalised,
+// and form the next four's dot products, beside the present four.  A group's rows
+// are interleaved, so that the groups' 16-byte reads of k and q meet in no bank.
+template <int R, bool BF16, int W>
+__global__ void __launch_bounds__(W * 32, R == 16 ? 12 / W : 1) recurrent_ragged_kernel(const PoolParams p) {
+    constexpr int kDk = R * kGroups, kThreads = W * 32, kWide = W * kCols;
+    constexpr int kRun = R < 4 ? R : 4;              // consecutive rows
+    constexpr int kMine = kFour / W;                 // tokens a warp brings
+    constexpr int kPer = (kDk + 31) / 32, kPerV = kWide / 32;   // numbers of k, v a lane brings
+    constexpr int kDot = kThreads / 16;              // threads that share a dot product
+    __shared__ __align__(16) float ks[3][kFour][kDk], qs[3][kFour][kDk], vs[3][kFour][kWide];
+    __shared__ __align__(16) float alphas[3][kFour], betas[3][kFour], kk[2][kFour][kFour], kq[2][kFour][kFour];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slices = p.dv / kWide;
+    const int slice = blockIdx.x % slices, h = blockIdx.x / slices % p.H;
+    int s = blockIdx.x / slices / p.H;
+    if (p.rows / 16 >= p.seqs) s = longest_first<kThreads>(p, s);
+    int slot, begin, end;
+    if (!sequence(p, s, &slot, &begin, &end)) return;
+    if (slot < 0) {                      // no sequence: zero rows of o
+        for (int64_t t = begin; t < end; ++t)
+            if (threadIdx.x < kWide) store_o(p, (t * p.H + h) * p.dv + slice * kWide + threadIdx.x, 0.f);
+        return;
+    }
+    const int group = lane >> 2, quad = lane & 3, hk = h / (p.H / p.Hk);
+    auto row_of = [&](int r) { return (group + kGroups * (r / kRun)) * kRun + r % kRun; };
+    const int col0 = slice * kWide + warp * kCols;
+    float4 *hp = reinterpret_cast<float4 *>(p.state + ((int64_t)slot * p.H + h) * p.dk * p.dv + col0) + quad;
+    const int pitch = p.dv / 4;          // float4 a row
+    F2 g[R / 2][4];
+
+    // this warp's tokens of a four, from memory (zeros behind the end): kPer consecutive
+    // numbers of q and k a lane, kPerV of v
+    Raw<kPer, BF16> kr[kMine], qr[kMine];
+    Raw<kPerV, BF16> vr[kMine];
+    float ar[kMine], br[kMine];
+    const int in_row = lane * kPer, in_v = lane * kPerV;
+    const int64_t ko = (int64_t)hk * p.k_head + in_row, qo = (int64_t)hk * p.q_head + in_row;
+    const int64_t vo = (int64_t)h * p.v_head + slice * kWide + in_v;
+    auto fetch = [&](int n) {
+#pragma unroll
+        for (int m = 0; m < kMine; ++m) {
+            const int64_t t = (int64_t)begin + n * kFour + warp + m * W;
+            kr[m].zero(); qr[m].zero(); vr[m].zero();
+            ar[m] = br[m] = 1.f;
+            if (t < end) {
+                if (in_row < kDk) {
+                    if (p.vec) {
+                        kr[m].template load<true>(p.k, t * p.k_row + ko);
+                        qr[m].template load<true>(p.q, t * p.q_row + qo);
+                    } else {
+                        kr[m].template load<false>(p.k, t * p.k_row + ko);
+                        qr[m].template load<false>(p.q, t * p.q_row + qo);
+                    }
+                }
+                if (p.vec) vr[m].template load<true>(p.v, t * p.v_row + vo);
+                else vr[m].template load<false>(p.v, t * p.v_row + vo);
+                if (p.alpha) ar[m] = __ldg(p.alpha + t * p.alpha_row + h);
+                if (p.beta) br[m] = __ldg(p.beta + t * p.beta_row + h);
+            }
+        }
+    };
+    auto keep = [&](int b) {
+#pragma unroll
+        for (int m = 0; m < kMine; ++m) {
+            const int i0 = warp + m * W;
+            float k[kPer], q[kPer], v[kPerV];
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) { k[i] = kr[m].get(i); q[i] = qr[m].get(i); }
+#pragma unroll
+            for (int i = 0; i < kPerV; ++i) v[i] = vr[m].get(i);
+            if (p.qk_norm) {
+                float x = 0.f, y = 0.f;
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) { x = fmaf(k[i], k[i], x); y = fmaf(q[i], q[i], y); }
+#pragma unroll
+                for (int z = 1; z < 32; z *= 2) { x = xor_add(x, z); y = xor_add(y, z); }
+                x = 1.f / sqrtf(x + p.qk_eps);
+                y = 1.f / sqrtf(y + p.qk_eps);
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) { k[i] *= x; q[i] *= y; }
+            }
+            if (in_row < kDk) {
+                store_few<kPer>(&ks[b][i0][in_row], k);
+                store_few<kPer>(&qs[b][i0][in_row], q);
+            }
+            store_few<kPerV>(&vs[b][i0][in_v], v);
+            if (lane == 0) { alphas[b][i0] = ar[m]; betas[b][i0] = br[m]; }
+        }
+    };
+    // 6 products k_i . k_j (j < i) and 10 q_i . k_j (j <= i), kDot threads each
+    const int dot = threadIdx.x / kDot, part = threadIdx.x % kDot, de = dot < 6 ? dot : dot - 6;
+    const int dot_i0 = de < 1 ? 0 : de < 3 ? 1 : de < 6 ? 2 : 3, dot_j = de - dot_i0 * (dot_i0 + 1) / 2;
+    const int dot_i = dot < 6 ? dot_i0 + 1 : dot_i0;
+    auto dots = [&](int b, int to) {
+        const float *x = dot < 6 ? ks[b][dot_i] : qs[b][dot_i], *y = ks[b][dot_j];
+        float sum = 0.f;
+        if constexpr (kDk >= 4 * kDot) {
+#pragma unroll
+            for (int m = 0; m < kDk / 4 / kDot; ++m) {
+                const float4 u = reinterpret_cast<const float4 *>(x)[part + m * kDot], v = reinterpret_cast<const float4 *>(y)[part + m * kDot];
+                sum = fmaf(u.x, v.x, fmaf(u.y, v.y, fmaf(u.z, v.z, fmaf(u.w, v.w, sum))));
+            }
+        } else {
+#pragma unroll
+            for (int m = 0; m < kDk / kDot; ++m) sum = fmaf(x[part + m * kDot], y[part + m * kDot], sum);
+        }
+#pragma unroll
+        for (int m = 1; m < kDot; m *= 2) sum = xor_add(sum, m);
+        if (part == 0) (dot < 6 ? kk : kq)[to][dot_i][dot_j] = sum;
+    };
+    auto rows_at = [&](const float *x, F2 (&y)[R / 2]) {
+#pragma unroll
+        for (int r = 0; r < R; r += kRun) {
+            if constexpr (kRun == 4) {
+                const float4 z = *reinterpret_cast<const float4 *>(x + row_of(r));
+                y[r / 2] = pack(z.x, z.y);
+                y[r / 2 + 1] = pack(z.z, z.w);
+            } else {
+                const float2 z = *reinterpret_cast<const float2 *>(x + row_of(r));
+                y[r / 2] = pack(z.x, z.y);
+            }
+        }
+    };
+    // this lane's sums over its rows of g with one token's numbers, by column
+    auto partial = [&](const float *x, float (&y)[4]) {
+        F2 xp[R / 2], acc[4];
+        rows_at(x, xp);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[c] = mul2(g[0][c], xp[0]);
+#pragma unroll
+        for (int r = 1; r < R / 2; ++r)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[c] = fma2(g[r][c], xp[r], acc[c]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) y[c] = both(acc[c]);
+    };
+    // halving exchange over bits 4 and 3: the sum of column 2 (bit 4) + (bit 3)
+    const bool hi = lane & 16, odd = lane & 8, is_q = lane & 4;
+    auto halve = [&](const float (&y)[4]) {
+        const float a = (hi ? y[2] : y[0]) + __shfl_xor_sync(~0u, hi ? y[0] : y[2], 16);
+        const float c = (hi ? y[3] : y[1]) + __shfl_xor_sync(~0u, hi ? y[1] : y[3], 16);
+        return (odd ? c : a) + __shfl_xor_sync(~0u, odd ? a : c, 8);
+    };
+
+    const int mine = warp * kCols + quad * 4 + 2 * hi + odd;      // the lane's column after it
+    const int64_t o_row = (int64_t)p.H * p.dv;
+    int64_t oi = ((int64_t)begin * p.H + h) * p.dv + slice * kWide + mine;
+    float A = 1.f;
+
+    // `cnt` tokens from token i0 of the four in buffer b, with products in buffer d;
+    // Ai: the decays up to each of them.  ALL: cnt = 4, i0 = 0.
+    auto advance = [&](auto all, int b, int d, int i0, int cnt, const float (&Ai)[kFour]) {
+        constexpr bool ALL = decltype(all)::value;
+        if (ALL) i0 = 0;
+        auto has = [&](int i) { return ALL || i < cnt; };
+        float sum[kFour], u[kFour];      // P in the lanes with bit 2 clear, Q in those with it set
+#pragma unroll
+        for (int i = 0; i < kFour; ++i) {
+            float P[4] = {0.f, 0.f, 0.f, 0.f}, Q[4] = {0.f, 0.f, 0.f, 0.f};
+            if (has(i)) { partial(ks[b][i0 + i], P); partial(qs[b][i0 + i], Q); }
+            const float x = halve(P), y = halve(Q);
+            sum[i] = (is_q ? y : x) + __shfl_xor_sync(~0u, is_q ? x : y, 4);
+        }
+        // u' where P is, then across to where Q is
+#pragma unroll
+        for (int i = 0; i < kFour; ++i) {
+            float y = sum[i];
+#pragma unroll
+            for (int j = 0; j < i; ++j)
+                if (has(i)) y = fmaf(kk[d][i0 + i][i0 + j], u[j], y);
+            u[i] = has(i) ? betas[b][i0 + i] * (__fdividef(vs[b][i0 + i][mine], Ai[i]) - y) : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < kFour; ++i) {
+            const float y = __shfl_xor_sync(~0u, u[i], 4);
+            if (is_q) u[i] = y;
+        }
+#pragma unroll
+        for (int i = 0; i < kFour; ++i)
+            if (has(i)) {
+                float y = sum[i];
+#pragma unroll
+                for (int j = 0; j <= i; ++j) y = fmaf(kq[d][i0 + i][i0 + j], u[j], y);
+                if (is_q) store_o(p, oi, Ai[i] * y);
+                oi += o_row;
+            }
+#pragma unroll
+        for (int i = 0; i < kFour; ++i) {
+            const float un = __shfl_xor_sync(~0u, u[i], 8);
+            const float u0 = odd ? un : u[i], u1 = odd ? u[i] : un;
+            const float w0 = __shfl_xor_sync(~0u, u0, 16), w1 = __shfl_xor_sync(~0u, u1, 16);
+            const float y[4] = {hi ? w0 : u0, hi ? w1 : u1, hi ? u0 : w0, hi ? u1 : w1};
+            if (has(i)) {
+                F2 kp[R / 2];
+                rows_at(ks[b][i0 + i], kp);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const F2 uu = pack(y[c], y[c]);
+#pragma unroll
+                    for (int r = 0; r < R / 2; ++r) g[r][c] = fma2(kp[r], uu, g[r][c]);
+                }
+            }
+        }
+    };
+    auto in = [](float x, float lo, float hi) { return x > lo && x < hi; };
+    auto into_g = [&](float x) {
+        const F2 f = pack(x, x);
+#pragma unroll
+        for (int r = 0; r < R / 2; ++r)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) g[r][c] = mul2(g[r][c], f);
+    };
+
+    const int fours = (end - begin + kFour - 1) / kFour;
+    fetch(0);                            // before the state: it is needed first
+    float4 rows[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) rows[r] = __ldcg(hp + row_of(r) * pitch);
+    keep(0);
+    if (fours > 1) { fetch(1); keep(1); }
+    if (fours > 2) fetch(2);
+#pragma unroll
+    for (int r = 0; r < R; r += 2) {
+        g[r / 2][0] = pack(rows[r].x, rows[r + 1].x); g[r / 2][1] = pack(rows[r].y, rows[r + 1].y);
+        g[r / 2][2] = pack(rows[r].z, rows[r + 1].z); g[r / 2][3] = pack(rows[r].w, rows[r + 1].w);
+    }
+    __syncthreads();
+    dots(0, 0);
+    __syncthreads();
+    int b = 0;                           // n % 3
+    for (int n = 0; n < fours; ++n) {
+        const int next = b == 2 ? 0 : b + 1, after = next == 2 ? 0 : next + 1;
+        // four n + 2, fetched one four ago, takes the place of four n - 1
+        if (n + 2 < fours) keep(after);
+        if (n + 3 < fours) fetch(n + 3);
+        const int tokens = min(kFour, end - begin - n * kFour);
+        constexpr float kLo = 2.3283064e-10f, kHi = 4.2949673e9f, kLo2 = 5.4210109e-20f, kHi2 = 1.8446744e19f;   // 2^-+32, 2^-+64
+        float Ai[kFour];
+        Ai[0] = A * alphas[b][0];
+#pragma unroll
+        for (int i = 1; i < kFour; ++i) Ai[i] = Ai[i - 1] * alphas[b][i];
+        if (tokens == kFour && in(Ai[0], kLo, kHi) && in(Ai[1], kLo2, kHi2) && in(Ai[2], kLo2, kHi2) && in(Ai[3], kLo2, kHi2)) {
+            advance(std::true_type(), b, n & 1, 0, kFour, Ai);
+            A = Ai[3];
+        } else {
+            for (int i0 = 0, cnt; i0 < tokens; i0 += cnt) {
+                Ai[0] = A * alphas[b][i0];
+                if (!in(Ai[0], kLo, kHi)) { into_g(Ai[0]); Ai[0] = 1.f; }
+                A = Ai[0];
+                cnt = 1;
+#pragma unroll
+                for (int i = 1; i < kFour; ++i) {
+                    Ai[i] = 1.f;
+                    if (cnt == i && i0 + i < tokens) {
+                        const float x = Ai[i - 1] * alphas[b][i0 + i];
+                        if (in(x, kLo2, kHi2)) { Ai[i] = A = x; cnt = i + 1; }
+                    }
+                }
+                advance(std::false_type(), b, n & 1, i0, cnt, Ai);
+            }
+        }
+        if (n + 1 < fours) dots(next, (n + 1) & 1);
+        __syncthreads();
+        b = next;
+    }
+#pragma unroll
+    for (int r = 0; r < R; r += 2) {
+        float x[4], y[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) unpack(g[r / 2][c], &x[c], &y[c]);
+        __stcg(hp + row_of(r) * pitch, make_float4(A * x[0], A * x[1], A * x[2], A * x[3]));
+        __stcg(hp + row_of(r + 1) * pitch, make_float4(A * y[0], A * y[1], A * y[2], A * y[3]));
+    }
+}
+
+template <int R, bool BF16>
+void launch_r(const PoolParams &p, cudaStream_t stream) {
+    unsigned blocks = (unsigned)p.seqs * (unsigned)p.H;
+    if (p.cu_seqlens) {
+        if (p.dv % 64 == 0) recurrent_ragged_kernel<R, BF16, 4><<<blocks * (p.dv / 64), 128, 0, stream>>>(p);
+        else recurrent_ragged_kernel<R, BF16, 2><<<blocks * (p.dv / 32), 64, 0, stream>>>(p);
+    } else if (p.vec) recurrent_step_kernel<R, BF16, true><<<blocks, p.dv / 4 * kGroups, 0, stream>>>(p);
+    else recurrent_step_kernel<R, BF16, false><<<blocks, p.dv / 4 * kGroups, 0, stream>>>(p);
+}
+template <int R>
+void launch_io(const PoolParams &p, cudaStream_t stream) {
+    if (p.io_bf16) launch_r<R, true>(p, stream);
+    else launch_r<R, false>(p, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_recurrent_pool(const PoolParams &p, cudaStream_t stream) {
-    const int64_t items = (int64_t)p.seqs * p.H * (p.dv / kCols);
-    const unsigned blocks = (unsigned)((items + kWarps - 1) / kWarps);
     switch (p.dk / kGroups) {
-        case 2: launch_r<2>(p, blocks, stream); break;
-        case 4: launch_r<4>(p, blocks, stream); break;
-        case 8: launch_r<8>(p, blocks, stream); break;
-        case 16: launch_r<16>(p, blocks, stream); break;
+        case 2: launch_io<2>(p, stream); break;
+        case 4: launch_io<4>(p, stream); break;
+        case 8: launch_io<8>(p, stream); break;
+        case 16: launch_io<16>(p, stream); break;
         default: return cudaErrorInvalidValue;
     }
     return cudaGetLastError();

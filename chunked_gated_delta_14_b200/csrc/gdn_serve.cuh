@@ -11,7 +11,7 @@ namespace gdn {
 
 struct PoolParams {
     int rows, seqs, H, Hk, dk, dv, pool;
-    int io_bf16, o_bf16, qk_norm, vec;   // vec: q, k rows start on 16 bytes
+    int io_bf16, o_bf16, qk_norm, vec;   // vec: every row of q, k, v starts on 16 bytes
     float qk_eps;
     const void *q, *k, *v;
     int64_t q_row, q_head, k_row, k_head, v_row, v_head;

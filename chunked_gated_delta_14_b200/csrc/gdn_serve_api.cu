@@ -48,8 +48,7 @@ gdn_status resolve_pool(const gdn_recurrent_args *a, gdn::PoolParams *out) {
     if (a->q_row < 0 || a->q_head < 0 || a->k_row < 0 || a->k_head < 0 || a->v_row < 0 || a->v_head < 0 ||
         a->alpha_row < 0 || a->beta_row < 0)
         return api_fail(GDN_ERR_INVALID_ARG, "strides must be >= 0");
-    if ((int64_t)a->seqs * a->H * (a->dv / 16) > (int64_t)4 * 0x7fffffff)
-        return api_fail(GDN_ERR_INVALID_ARG, "seqs * H * dv too large");
+    if ((int64_t)a->seqs * a->H > 0x7fffffff / 4) return api_fail(GDN_ERR_INVALID_ARG, "seqs * H too large");
     if (a->seqs > 0 && a->rows > 0) {
         if (!a->q || !a->k || !a->v || !a->o || !a->state)
             return api_fail(GDN_ERR_INVALID_ARG, "q, k, v, state and o are required");
@@ -77,7 +76,8 @@ gdn_status resolve_pool(const gdn_recurrent_args *a, gdn::PoolParams *out) {
     p.alpha = a->alpha; p.beta = a->beta; p.alpha_row = a->alpha_row; p.beta_row = a->beta_row;
     p.cu_seqlens = a->cu_seqlens; p.slots = a->slots; p.state = a->state; p.o = a->o;
     const int64_t unit = 16 / size_of(a->io_dtype);
-    p.vec = on16(a->q) && on16(a->k) && !(a->q_row % unit) && !(a->q_head % unit) && !(a->k_row % unit) && !(a->k_head % unit);
+    p.vec = on16(a->q) && on16(a->k) && on16(a->v) && !(a->q_row % unit) && !(a->q_head % unit) && !(a->k_row % unit) &&
+            !(a->k_head % unit) && !(a->v_row % unit) && !(a->v_head % unit);
     *out = p;
     return GDN_OK;
 }

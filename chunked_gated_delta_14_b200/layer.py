@@ -59,7 +59,11 @@ def _packer(mirror):
 
 _pack_recurrent, _pack_rows, _pack_matmul = (_packer(m) for m in (RecurrentArgs, RowsArgs, Int8MatmulArgs))
 _DTYPES = {torch.float32: GDN_F32, torch.bfloat16: GDN_BF16}
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_functions = {}
+# torch.cuda.current_stream(i).cuda_stream and current_device(), without their objects (2 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_empty = torch.empty_strided          # a third quicker than torch.empty
 
 
 def _check(t, name, shape, dtypes, device):
@@ -88,6 +92,13 @@ def _first(t, name, dims, dtypes):
     _check(t, name, t.shape, dtypes, t.device)
 
 
+def _fits(t, shape, dtype, i, grad):
+    """Whether a tensor is what ``_check`` lets pass but for its strides, quickly (the checks are
+    most of what a small call costs); where it is not, ``_check`` says what is wrong, or lets it
+    pass.  ``grad``: whether gradients are recorded."""
+    return t.shape == shape and t.dtype is dtype and t.get_device() == i and not (grad and t.requires_grad)
+
+
 _IO = (torch.bfloat16, torch.float32)
 _F32, _I32, _I8 = (torch.float32,), (torch.int32,), (torch.int8,)
 
@@ -95,7 +106,7 @@ _F32, _I32, _I8 = (torch.float32,), (torch.int32,), (torch.int8,)
 def _rows(t, name):
     """(rows, stride) of t seen as rows of its last dimension."""
     if t.dim() == 2:
-        return t.shape[0], t.stride(0)
+        return t.shape[0], t.stride()[0]
     try:
         t = t.view(-1, t.shape[-1])
     except RuntimeError:
@@ -116,10 +127,10 @@ def _other_stream(stream, device, tensors, call):
     return r
 
 
-def _launch(fn, packed, device):
-    """Raw call on the device's current stream; raises GDNError on a non-OK status."""
-    i = device.index
-    if torch.cuda.current_device() == i:
+def _launch(name, packed, i):
+    """Raw call on device i's current stream; raises GDNError on a non-OK status."""
+    fn = _functions.get(name) or _functions.setdefault(name, getattr(lib(), name))
+    if _current_device() == i:
         s = fn(packed, _raw_stream(i))
     else:
         with torch.cuda.device(i):
@@ -181,45 +192,69 @@ def recurrent_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, alpha: Opti
     if stream is not None:
         return _other_stream(stream, q.device, (q, k, v, alpha, beta, state, slots, cu_seqlens, out), lambda: recurrent_fwd(
             q, k, v, alpha, beta, state, slots, cu_seqlens, qk_norm_eps=qk_norm_eps, o_dtype=o_dtype, out=out))
-    _first(q, "q", 3, _IO)
-    dev, io = q.device, (q.dtype,)
-    if q.dim() != 3 or not isinstance(v, torch.Tensor) or v.dim() != 3:
-        raise ValueError("q must be [N, Hk, dk] and v [N, H, dv]")
+    _tensors(q=q, k=k, v=v, state=state)
+    if q.dim() != 3 or v.dim() != 3 or state.dim() != 4:
+        raise ValueError("q must be [N, Hk, dk], v [N, H, dv] and state [P, H, dk, dv]")
+    io, i, grad = q.dtype, q.get_device(), torch.is_grad_enabled()
     N, Hk, dk = q.shape
-    H, dv = v.shape[1:]
-    _check(k, "k", q.shape, io, dev)
-    _check(v, "v", (N, H, dv), io, dev)
-    if alpha is not None:
-        _check(alpha, "alpha", (N, H), _F32, dev)
-    if beta is not None:
-        _check(beta, "beta", (N, H), _F32, dev)
-    if not isinstance(state, torch.Tensor) or state.dim() != 4:
-        raise ValueError("state must be [P, H, dk, dv]")
-    _check(state, "state", (state.shape[0], H, dk, dv), _F32, dev)
-    if not state.is_contiguous():
-        raise ValueError("state must be contiguous")
-    S = N
+    _, H, dv = v.shape
+    P = state.shape[0]
+    S, dev = N, q.device
     if cu_seqlens is not None:
-        if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        _tensors(cu_seqlens=cu_seqlens)
+        if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
             raise ValueError("cu_seqlens must be [S + 1]")
         S = cu_seqlens.shape[0] - 1
-        _check(cu_seqlens, "cu_seqlens", (S + 1,), _I32, dev)
+        if not _fits(cu_seqlens, (S + 1,), torch.int32, i, grad) or cu_seqlens.stride()[0] != 1:
+            _check(cu_seqlens, "cu_seqlens", (S + 1,), _I32, dev)
+    (qr, qh, q1), (kr, kh, k1), (vr, vh, v1) = q.stride(), k.stride(), v.stride()
+    if not (i >= 0 and io in _DTYPES and _fits(q, q.shape, io, i, grad) and _fits(k, q.shape, io, i, grad) and _fits(v, (N, H, dv), io, i, grad)
+            and q1 == k1 == v1 == 1):
+        _first(q, "q", 3, _IO)
+        _check(k, "k", q.shape, (io,), dev)
+        _check(v, "v", (N, H, dv), (io,), dev)
+    if not _fits(state, (P, H, dk, dv), torch.float32, i, grad):
+        _check(state, "state", (P, H, dk, dv), _F32, dev)
+    if not state.is_contiguous():
+        raise ValueError("state must be contiguous")
+    ap = bp = ar = br = cp = sp = 0
+    if alpha is not None:
+        _tensors(alpha=alpha)
+        if not _fits(alpha, (N, H), torch.float32, i, grad) or alpha.stride()[1] != 1:
+            _check(alpha, "alpha", (N, H), _F32, dev)
+        ap, ar = alpha.data_ptr(), alpha.stride()[0]
+    if beta is not None:
+        _tensors(beta=beta)
+        if not _fits(beta, (N, H), torch.float32, i, grad) or beta.stride()[1] != 1:
+            _check(beta, "beta", (N, H), _F32, dev)
+        bp, br = beta.data_ptr(), beta.stride()[0]
     if slots is not None:
-        _check(slots, "slots", (S,), _I32, dev)
+        _tensors(slots=slots)
+        if not _fits(slots, (S,), torch.int32, i, grad) or slots.stride()[0] != 1:
+            _check(slots, "slots", (S,), _I32, dev)
+        sp = slots.data_ptr()
+    if cu_seqlens is not None:
+        cp = cu_seqlens.data_ptr()
     if out is None:
         make = torch.empty if cu_seqlens is None else torch.zeros
-        out = make((N, H, dv), device=dev, dtype=o_dtype or q.dtype)
-    _check(out, "out", (N, H, dv), _IO if o_dtype is None else (o_dtype,), dev)
-    if not out.is_contiguous():
-        raise ValueError("out must be contiguous")
-    opt = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
-    (qr, qh, _), (kr, kh, _), (vr, vh, _) = q.stride(), k.stride(), v.stride()
-    _launch(lib().gdn_recurrent_fwd, _pack_recurrent(
-        N, S, H, Hk, dk, dv, state.shape[0], _DTYPES[q.dtype], _code(out.dtype), int(qk_norm_eps is not None),
-        qk_norm_eps or 0.0, q.data_ptr(), k.data_ptr(), v.data_ptr(), qr, qh, kr, kh, vr, vh, opt(alpha), opt(beta),
-        0 if alpha is None else alpha.stride(0), 0 if beta is None else beta.stride(0), opt(cu_seqlens), opt(slots),
-        state.data_ptr(), out.data_ptr()), dev)
+        out = make((N, H, dv), device=dev, dtype=o_dtype or io)
+    else:
+        _tensors(out=out)
+        if not _fits(out, (N, H, dv), o_dtype or out.dtype, i, grad):
+            _check(out, "out", (N, H, dv), (o_dtype or out.dtype,), dev)
+        if not out.is_contiguous():
+            raise ValueError("out must be contiguous")
+    _launch("gdn_recurrent_fwd", _pack_recurrent(
+        N, S, H, Hk, dk, dv, P, _DTYPES[io], _code(out.dtype), 0 if qk_norm_eps is None else 1, qk_norm_eps or 0.0,
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), qr, qh, kr, kh, vr, vh, ap, bp, ar, br, cp, sp, state.data_ptr(),
+        out.data_ptr()), i)
     return out
+
+
+def _tensors(**named):
+    for name, t in named.items():
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
 
 
 def _code(dt):
@@ -229,11 +264,13 @@ def _code(dt):
 
 
 def _steps(lead, rows, width, dev):
-    """A tensor [*lead, width] of int8 whose rows start on 16 bytes, and its row stride."""
+    """Rows of int8 [*lead, width] that start on 16 bytes, their stride, and their scales [*lead]."""
     pitch = (width + 15) // 16 * 16
-    if pitch == width:
-        return torch.empty((*lead, width), device=dev, dtype=torch.int8), pitch
-    return torch.empty((*lead, pitch), device=dev, dtype=torch.int8)[..., :width], pitch
+    if len(lead) == 1:
+        return (_empty((rows, width), (pitch, 1), device=dev, dtype=torch.int8), pitch,
+                _empty((rows,), (1,), device=dev, dtype=torch.float32))
+    q = torch.empty((*lead, pitch), device=dev, dtype=torch.int8)
+    return q if pitch == width else q[..., :width], pitch, torch.empty(lead, device=dev, dtype=torch.float32)
 
 
 def add_rms_norm_int8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None, *,
@@ -251,35 +288,57 @@ def add_rms_norm_int8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, re
     if stream is not None:
         return _other_stream(stream, x.device, (x, weight, residual, residual_out), lambda: add_rms_norm_int8(
             x, weight, residual, eps=eps, residual_out=residual_out))
-    _first(x, "x", 1, _IO)
-    dev, D = x.device, x.shape[-1]
+    i, grad, xd = _row_input(x, 1)
+    shape, dev = x.shape, x.device
+    D = shape[-1]
     rows, xr = _rows(x, "x")
     rr = ror = rdt = wdt = rp = wp = rop = 0
     if weight is not None:
-        _check(weight, "weight", (D,), _IO, dev)
-        wdt, wp = _DTYPES[weight.dtype], weight.data_ptr()
+        wdt, wp = _row_weight(weight, (D,), i, grad, dev)
     if residual is not None:
-        _check(residual, "residual", x.shape, _IO, dev)
-        rdt, rp = _DTYPES[residual.dtype], residual.data_ptr()
-        rr = _rows(residual, "residual")[1]
+        _tensors(residual=residual)
+        rd = residual.dtype
+        if not (rd in _DTYPES and _fits(residual, shape, rd, i, grad) and residual.stride()[-1] == 1):
+            _check(residual, "residual", shape, _IO, dev)
+        rdt, rp, rr = _DTYPES[rd], residual.data_ptr(), _rows(residual, "residual")[1]
         if residual_out is None:
-            residual_out = torch.empty(x.shape, device=dev, dtype=residual.dtype)
-        _check(residual_out, "residual_out", x.shape, (residual.dtype,), dev)
+            residual_out = _empty(shape, (D, 1), device=dev, dtype=rd) if len(shape) == 2 else torch.empty(shape, device=dev, dtype=rd)
+        else:
+            _tensors(residual_out=residual_out)
+            _check(residual_out, "residual_out", shape, (rd,), dev)
         rop, ror = residual_out.data_ptr(), _rows(residual_out, "residual_out")[1]
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
-    lead = x.shape[:-1]
-    q, qr = _steps(lead, rows, D, dev)
-    scale = torch.empty(lead, device=dev, dtype=torch.float32)
-    _launch(lib().gdn_rows_int8, _pack_rows(ROWS_NORM, rows, D, 0, _DTYPES[x.dtype], rdt, wdt, eps, x.data_ptr(), rp, 0, wp,
-                                            xr, rr, 0, ror, qr, rop, q.data_ptr(), scale.data_ptr()), dev)
+    q, qr, scale = _steps(shape[:-1], rows, D, dev)
+    _launch("gdn_rows_int8", _pack_rows(ROWS_NORM, rows, D, 0, xd, rdt, wdt, eps, x.data_ptr(), rp, 0, wp, xr, rr, 0, ror, qr,
+                                        rop, q.data_ptr(), scale.data_ptr()), i)
     return q, scale, residual_out
+
+
+def _row_input(x, dims):
+    """(device index, whether gradients are recorded, dtype code) of a checked x."""
+    _tensors(x=x)
+    i, grad, xd = x.get_device(), torch.is_grad_enabled(), _DTYPES.get(x.dtype)
+    if xd is None or i < 0 or x.dim() < dims or (grad and x.requires_grad) or x.stride()[-1] != 1:
+        _first(x, "x", dims, _IO)
+    return i, grad, xd
+
+
+def _row_weight(weight, shape, i, grad, dev):
+    _tensors(weight=weight)
+    wd = weight.dtype
+    if not (wd in _DTYPES and _fits(weight, shape, wd, i, grad) and weight.stride()[0] == 1):
+        _check(weight, "weight", shape, _IO, dev)
+    return _DTYPES[wd], weight.data_ptr()
 
 
 def _head_rows(t, name):
     """(rows, stride) of t [..., H, d] seen as rows of H * d."""
-    if t.dim() == 3 and (t.stride(1) == t.shape[2] or t.shape[1] == 1):
-        return t.shape[0], t.stride(0)
+    if t.dim() == 3:
+        rows, H, d = t.shape
+        row, head, _ = t.stride()
+        if head == d or H == 1:
+            return rows, row
     try:
         t = t.view(-1, t.shape[-2] * t.shape[-1])
     except RuntimeError:
@@ -297,20 +356,20 @@ def gated_rms_norm_int8(x: torch.Tensor, gate: torch.Tensor, weight: Optional[to
     int8, its rows on 16-byte boundaries; scale: [...] fp32, one for all heads of a row."""
     if stream is not None:
         return _other_stream(stream, x.device, (x, gate, weight), lambda: gated_rms_norm_int8(x, gate, weight, eps=eps))
-    _first(x, "x", 2, _IO)
+    i, grad, xd = _row_input(x, 2)
     dev = x.device
     *lead, H, d = x.shape
-    _check(gate, "gate", x.shape, (x.dtype,), dev)
+    _tensors(gate=gate)
+    if not (_fits(gate, x.shape, x.dtype, i, grad) and gate.stride()[-1] == 1):
+        _check(gate, "gate", x.shape, (x.dtype,), dev)
     wdt = wp = 0
     if weight is not None:
-        _check(weight, "weight", (d,), _IO, dev)
-        wdt, wp = _DTYPES[weight.dtype], weight.data_ptr()
+        wdt, wp = _row_weight(weight, (d,), i, grad, dev)
     rows, xr = _head_rows(x, "x")
     gr = _head_rows(gate, "gate")[1]
-    q, qr = _steps(lead, rows, H * d, dev)
-    scale = torch.empty(lead, device=dev, dtype=torch.float32)
-    _launch(lib().gdn_rows_int8, _pack_rows(ROWS_GATED, rows, H * d, d, _DTYPES[x.dtype], 0, wdt, eps, x.data_ptr(), 0,
-                                            gate.data_ptr(), wp, xr, 0, gr, 0, qr, 0, q.data_ptr(), scale.data_ptr()), dev)
+    q, qr, scale = _steps(lead, rows, H * d, dev)
+    _launch("gdn_rows_int8", _pack_rows(ROWS_GATED, rows, H * d, d, xd, 0, wdt, eps, x.data_ptr(), 0, gate.data_ptr(), wp, xr,
+                                        0, gr, 0, qr, 0, q.data_ptr(), scale.data_ptr()), i)
     return q, scale
 
 
@@ -320,14 +379,12 @@ def quantize_int8(x: torch.Tensor, *, stream: Optional[torch.cuda.Stream] = None
     whatever D is; scale: [...] fp32, the row's largest absolute value / 127."""
     if stream is not None:
         return _other_stream(stream, x.device, (x,), lambda: quantize_int8(x))
-    _first(x, "x", 1, _IO)
-    dev, D = x.device, x.shape[-1]
+    i, _, xd = _row_input(x, 1)
+    D = x.shape[-1]
     rows, xr = _rows(x, "x")
-    lead = x.shape[:-1]
-    q, qr = _steps(lead, rows, D, dev)
-    scale = torch.empty(lead, device=dev, dtype=torch.float32)
-    _launch(lib().gdn_rows_int8, _pack_rows(ROWS_PLAIN, rows, D, 0, _DTYPES[x.dtype], 0, 0, 0.0, x.data_ptr(), 0, 0, 0,
-                                            xr, 0, 0, 0, qr, 0, q.data_ptr(), scale.data_ptr()), dev)
+    q, qr, scale = _steps(x.shape[:-1], rows, D, x.device)
+    _launch("gdn_rows_int8", _pack_rows(ROWS_PLAIN, rows, D, 0, xd, 0, 0, 0.0, x.data_ptr(), 0, 0, 0, xr, 0, 0, 0, qr, 0,
+                                        q.data_ptr(), scale.data_ptr()), i)
     return q, scale
 
 
@@ -343,40 +400,52 @@ def int8_matmul(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale
     if stream is not None:
         return _other_stream(stream, x.device, (x, x_scale, w, w_scale, bias, out), lambda: int8_matmul(
             x, x_scale, w, w_scale, bias, out_dtype=out_dtype, out=out))
-    _first(x, "x", 1, _I8)
-    dev, K = x.device, x.shape[-1]
-    if not isinstance(w, torch.Tensor) or w.dim() != 2:
+    _tensors(x=x, x_scale=x_scale, w=w, w_scale=w_scale)
+    if w.dim() != 2:
         raise ValueError("w must be [N, K]")
-    N, lead = w.shape[0], x.shape[:-1]
-    _check(w, "w", (N, K), _I8, dev)
-    _check(w_scale, "w_scale", (N,), _F32, dev)
-    _check_scale(x_scale, lead, dev)
+    (N, wk), shape, i, grad, dev = w.shape, x.shape, x.get_device(), torch.is_grad_enabled(), x.device
+    if i < 0 or not len(shape) or x.dtype is not torch.int8 or x.stride()[-1] != 1:
+        _first(x, "x", 1, _I8)
+    lead, K = shape[:-1], shape[-1]
+    if not (wk == K and _fits(w, (N, K), torch.int8, i, False) and w.stride()[1] == 1):
+        _check(w, "w", (N, K), _I8, dev)
+    if not (_fits(w_scale, (N,), torch.float32, i, grad) and w_scale.stride()[0] == 1):
+        _check(w_scale, "w_scale", (N,), _F32, dev)
+    if not (_fits(x_scale, lead, torch.float32, i, grad) and x_scale.is_contiguous()):
+        _check_scale(x_scale, lead, dev)
+    bp = 0
     if bias is not None:
-        _check(bias, "bias", (N,), _F32, dev)
+        _tensors(bias=bias)
+        if not (_fits(bias, (N,), torch.float32, i, grad) and bias.stride()[0] == 1):
+            _check(bias, "bias", (N,), _F32, dev)
+        bp = bias.data_ptr()
     M, xr = _rows(x, "x")
+    od = _code(out_dtype)
     if out is None:
-        out = torch.empty((*lead, N), device=dev, dtype=out_dtype)
-    _check(out, "out", (*lead, N), (out_dtype,), dev)
-    wr, xp, wp = w.stride(0), x.data_ptr(), w.data_ptr()
-    fields = (M, N, K, _code(out_dtype), xp, wp, xr, wr, _rows(out, "out")[1], x_scale.data_ptr(), w_scale.data_ptr(),
-              0 if bias is None else bias.data_ptr(), out.data_ptr())
-    ws, need = None, 0
+        out = _empty((M, N), (N, 1), device=dev, dtype=out_dtype) if len(lead) == 1 else torch.empty((*lead, N), device=dev, dtype=out_dtype)
+        outr = N
+    else:
+        _tensors(out=out)
+        _check(out, "out", (*lead, N), (out_dtype,), dev)
+        outr = _rows(out, "out")[1]
+    wr, xp, wp = w.stride()[0], x.data_ptr(), w.data_ptr()
+    fields = (M, N, K, od, xp, wp, xr, wr, outr, x_scale.data_ptr(), w_scale.data_ptr(), bp, out.data_ptr())
+    ws = need = 0
     if (xp | wp | xr | wr) & 15 or not xr or not wr:
         # from torch's allocator and not kept: a call's copies belong to its stream, or its graph
         need = int8_matmul_workspace_bytes(Int8MatmulArgs(*fields))
-        ws = torch.empty(need, device=dev, dtype=torch.uint8) if need else None
-    _launch(lib().gdn_int8_matmul, _pack_matmul(*fields, 0 if ws is None else ws.data_ptr(), need), dev)
+        if need:
+            buffer = torch.empty(need, device=dev, dtype=torch.uint8)
+            ws = buffer.data_ptr()
+    _launch("gdn_int8_matmul", _pack_matmul(*fields, ws, need), i)
     return out
 
 
 def _check_scale(t, lead, dev):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("x_scale must be a torch.Tensor")
     if not t.is_contiguous():
         raise ValueError("x_scale must be contiguous")
     if t.dim() == 0:
         if len(lead):
             raise ValueError(f"x_scale has shape (), expected {tuple(lead)}")
-        t = t.view(1)
-        lead = (1,)
+        t, lead = t.view(1), (1,)
     _check(t, "x_scale", lead, _F32, dev)

@@ -150,6 +150,9 @@ class OnDevice(torch.Tensor):
     def device(self):
         return torch.device("cuda", 0)
 
+    def get_device(self):
+        return 0
+
 
 def dev(*shape, dtype=torch.float32, grad=False):
     return OnDevice(torch.zeros(*shape, dtype=dtype).requires_grad_(grad))

@@ -144,6 +144,38 @@ def test_recurrent_without_gates_and_with_unaligned_rows():
     check_rule(o, state, want, range(2), starts, q, 128, 5)
 
 
+@pytest.mark.parametrize("dk,dv", [(128, 128), (32, 96)])
+def test_recurrent_long_sequences_of_many_lengths(dk, dv):
+    """Lengths whose mean is over 16, where the blocks take the longest sequences first."""
+    g = torch.Generator().manual_seed(8)
+    lens = [1, 0, 200, 63, 64, 65, 2] + torch.randint(0, 60, (140,), generator=g).tolist()
+    slots = torch.randperm(160, generator=g)[:len(lens)].tolist()
+    slots[3] = slots[40] = -1
+    q, k, v, al, be, state, starts = make_rule(8, lens, 1, 1, dk, dv, F, pool=160, tail=4)
+    assert starts[-1] >= 16 * len(lens)
+    out = torch.full(v.shape, 5.0, device="cuda")
+    want = rule64(q, k, v, al, be, state, slots, starts, out)
+    gdn.recurrent_fwd(q, k, v, al, be, state, torch.tensor(slots, dtype=torch.int32, device="cuda"),
+                      torch.tensor(starts, dtype=torch.int32, device="cuda"), out=out)
+    gdn.device_check()
+    check_rule(out, state, want, slots, starts, q, dk, max(lens))
+    assert (out[starts[-1]:] == 5).all() and (out[starts[3]:starts[4]] == 0).all()
+
+
+@pytest.mark.parametrize("dk,dv", [(128, 128), (16, 32)])
+def test_recurrent_decays_of_any_size(dk, dv):
+    """Decays of 0 and near it, and long runs of small ones: no product of theirs is divided by."""
+    lens = [37, 13, 1, 1, 4]
+    q, k, v, al, be, state, starts = make_rule(9, lens, 1, 2, dk, dv, F)
+    g = rng(10)
+    pick = torch.tensor([0.0, 1e-38, 1e-30, 1e-12, 1e-6, 0.01, 0.5, 1.0], device="cuda")
+    al = pick[torch.randint(0, 8, al.shape, device="cuda", generator=g)]
+    al[starts[2]:starts[4]] = 0
+    want = rule64(q, k, v, al, be, state, range(5), starts, torch.zeros_like(v))
+    o = gdn.recurrent_fwd(q, k, v, al, be, state, None, torch.tensor(starts, dtype=torch.int32, device="cuda"))
+    check_rule(o, state, want, range(5), starts, q, dk, max(lens))
+
+
 def test_recurrent_equals_the_chunked_pass_and_takes_its_state():
     """A prompt through chunk_fwd, its final state written into the pool, then single tokens."""
     g, T, H = rng(5), 70, 2
