@@ -1,0 +1,33 @@
+// Two floats that one instruction works on (sm_100: fma.rn.f32x2 and its like).
+#pragma once
+
+#include <stdint.h>
+
+namespace gdn {
+
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 pack(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack(F2 x, float *lo, float *hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(*lo), "=f"(*hi) : "l"(x.v)); }
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ float both(F2 x) {
+    float lo, hi;
+    unpack(x, &lo, &hi);
+    return lo + hi;
+}
+
+}  // namespace gdn

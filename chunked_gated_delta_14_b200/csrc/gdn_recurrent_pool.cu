@@ -10,6 +10,7 @@
 
 #include <type_traits>
 
+#include "f32x2.cuh"
 #include "gdn_serve.cuh"
 
 namespace gdn {
@@ -174,32 +175,6 @@ __global__ void __launch_bounds__(256, 2) recurrent_step_kernel(const PoolParams
         store_o(p, oi + 2, fmaf(b, u[2], aq * y.z));
         store_o(p, oi + 3, fmaf(b, u[3], aq * y.w));
     }
-}
-
-// Two floats that one instruction works on (fma.rn.f32x2).
-struct F2 {
-    uint64_t v;
-};
-__device__ __forceinline__ F2 pack(float lo, float hi) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void unpack(F2 x, float *lo, float *hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(*lo), "=f"(*hi) : "l"(x.v)); }
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ float both(F2 x) {
-    float lo, hi;
-    unpack(x, &lo, &hi);
-    return lo + hi;
 }
 
 __device__ __forceinline__ float xor_add(float x, int mask) { return x + __shfl_xor_sync(~0u, x, mask); }

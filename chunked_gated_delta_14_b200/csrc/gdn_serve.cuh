@@ -27,7 +27,8 @@ struct RowsParams {
     int op, rows, width, head;
     int x_bf16, residual_bf16, weight_bf16;
     int vec;                             // every row starts on 16 bytes, width a multiple of 8
-    float eps;
+    int weight_vec, q_vec;               // the weight starts on 16 bytes, every row of q on 8
+    float eps, inverse;                  // inverse: 1 / the numbers a norm is of
     const void *x, *residual, *gate, *weight;
     int64_t x_row, residual_row, gate_row, residual_out_row, q_row;
     void *residual_out;
@@ -44,9 +45,15 @@ struct Int8MatmulParams {
     void *out;
 };
 cudaError_t launch_int8_matmul(const Int8MatmulParams &p, cudaStream_t stream, const char **why);
-// Rows of K bytes at any stride -> rows at stride `to_row` (a multiple of 16).
-cudaError_t launch_int8_pad_rows(const int8_t *from, int64_t from_row, int8_t *to, int64_t to_row, int rows, int K,
-                                 cudaStream_t stream);
+// Rows at any stride -> rows at stride `to_row` (a multiple of 16), of both operands at once.
+struct PadRows {
+    const int8_t *from;
+    int64_t from_row;
+    int8_t *to;
+    int64_t to_row;
+    int rows;           // 0: none
+};
+cudaError_t launch_int8_pad_rows(const PadRows &x, const PadRows &w, int K, cudaStream_t stream);
 
 // Return (and clear) the error word of these kernels; the caller has synchronised.
 unsigned int pool_read_and_clear_error(cudaError_t *err);

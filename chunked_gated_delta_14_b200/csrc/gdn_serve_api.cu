@@ -130,15 +130,17 @@ gdn_status resolve_rows(const gdn_rows_args *a, gdn::RowsParams *out) {
     gdn::RowsParams p{};
     p.op = a->op; p.rows = a->rows; p.width = a->width; p.head = gated ? a->head : 1;
     p.x_bf16 = a->x_dtype == GDN_BF16; p.residual_bf16 = a->residual_dtype == GDN_BF16; p.weight_bf16 = a->weight_dtype == GDN_BF16;
-    p.eps = a->eps;
+    p.eps = a->eps; p.inverse = 1.f / (float)(gated ? a->head : a->width);
     p.x = a->x; p.residual = a->residual; p.gate = a->gate; p.weight = a->weight;
     p.x_row = a->x_row; p.residual_row = a->residual_row; p.gate_row = a->gate_row;
     p.residual_out_row = a->residual_out_row; p.q_row = a->q_row;
     p.residual_out = a->residual_out; p.q = a->q; p.scale = a->scale;
     const auto rows16 = [](const void *ptr, int64_t row, int64_t size) { return !ptr || (on16(ptr) && row * size % 16 == 0); };
+    p.weight_vec = on16(a->weight);
+    p.q_vec = on(a->q, 8) && (a->q_row % 8 == 0 || a->rows == 1);
     p.vec = a->width % 8 == 0 && rows16(a->x, a->x_row, xs) && rows16(a->residual, a->residual_row, rs) &&
             rows16(a->gate, a->gate_row, xs) && rows16(a->residual_out, a->residual_out_row, rs) &&
-            rows16(a->weight, 0, ws) && on(a->q, 8) && a->q_row % 8 == 0;
+            p.weight_vec && p.q_vec;
     *out = p;
     return GDN_OK;
 }
@@ -231,15 +233,17 @@ gdn_status gdn_int8_matmul(const gdn_int8_matmul_args *args, void *stream) {
         if (!on16(args->workspace)) return api_fail(GDN_ERR_ALIGNMENT, "the workspace must be 16-byte aligned");
         int8_t *to = static_cast<int8_t *>(args->workspace);
         const int64_t row = up16(m.p.K);
+        gdn::PadRows x{}, w{};
         if (m.copy_x) {
-            e = gdn::launch_int8_pad_rows(m.p.x, m.p.x_row, to, row, m.p.M, m.p.K, st);
+            x = {m.p.x, m.p.x_row, to, row, m.p.M};
             m.p.x = to; m.p.x_row = row;
             to += (int64_t)m.p.M * row;
         }
-        if (m.copy_w && e == cudaSuccess) {
-            e = gdn::launch_int8_pad_rows(m.p.w, m.p.w_row, to, row, m.p.N, m.p.K, st);
+        if (m.copy_w) {
+            w = {m.p.w, m.p.w_row, to, row, m.p.N};
             m.p.w = to; m.p.w_row = row;
         }
+        e = gdn::launch_int8_pad_rows(x, w, m.p.K, st);
     }
     const char *why = "";
     if (e == cudaSuccess) e = gdn::launch_int8_matmul(m.p, st, &why);

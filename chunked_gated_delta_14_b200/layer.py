@@ -252,8 +252,8 @@ def recurrent_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, alpha: Opti
 
 
 def _tensors(**named):
-    for name, t in named.items():
-        if not isinstance(t, torch.Tensor):
+    for name in named:
+        if not isinstance(named[name], torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
 
 
@@ -433,7 +433,7 @@ def int8_matmul(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale
     ws = need = 0
     if (xp | wp | xr | wr) & 15 or not xr or not wr:
         # from torch's allocator and not kept: a call's copies belong to its stream, or its graph
-        need = int8_matmul_workspace_bytes(Int8MatmulArgs(*fields))
+        need = lib().gdn_int8_matmul_workspace_bytes(_pack_matmul(*fields, 0, 0))
         if need:
             buffer = torch.empty(need, device=dev, dtype=torch.uint8)
             ws = buffer.data_ptr()

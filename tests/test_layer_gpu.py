@@ -369,7 +369,8 @@ def make_product(seed, M, N, K, pad=True, bias=False):
 @pytest.mark.parametrize("out_dtype", [BF, F])
 @pytest.mark.parametrize("M,N,K", [(1, 1, 1), (1, 16, 16), (1, 129, 128), (2, 257, 2048), (16, 128, 127), (17, 300, 1537),
                                    (33, 1000, 129), (64, 513, 4096), (65, 128, 256), (127, 384, 640), (129, 257, 100),
-                                   (200, 1001, 1000), (300, 130, 8192), (513, 2050, 320), (700, 8224, 272)])
+                                   (200, 1001, 1000), (300, 130, 8192), (513, 2050, 320), (700, 8224, 272),
+                                   (16, 8224, 2048), (9, 8192, 130), (2300, 2100, 130), (3001, 2900, 257), (4200, 4100, 300)])
 def test_product(M, N, K, out_dtype):
     x, xs, w, ws, bias = make_product(20, M, N, K, bias=(M + N) % 2 == 0)
     out = gdn.int8_matmul(x, xs, w, ws, bias, out_dtype=out_dtype)
