@@ -12,7 +12,7 @@
 // positive and the same for the whole row, so NORM too has one exchange.  Beside
 // the bytes the instructions count (bf16 rows leave about 20 a number): everything
 // is loaded before anything is waited for, products and sums go two in an
-// instruction, and steps come from one fma instead of a conversion.
+// instruction, and steps come from a sum instead of a conversion.
 //
 // Measured, of the copy rate: NORM of 8192 x 4096 bf16 with an fp32 residual 57 us
 // (98%); PLAIN of 8224 x 2048 bf16 8.0 us (97%); GATED of 16384 rows of 16 heads of
@@ -162,12 +162,17 @@ __device__ __forceinline__ float scale_of(float top, float *factor) {
     if (!(top < __uint_as_float(kInfBits))) return __uint_as_float(0x7fc00000u);
     const float s = top * (1.f / 127.f);
     if (s < 1.17549435e-38f) return 0.f;
-    *factor = rcp(top * 0.0625f) * (127.f * 0.0625f);    // from 1.5e-36 to 3.4e38 both are normal
+    // 127 / top, one correction after an approximate reciprocal; with a sixteenth of both, which
+    // keeps the reciprocal normal for tops from 1.5e-36 to 3.4e38
+    const float t = top * 0.0625f, r = rcp(t), f = 7.9375f * r;
+    *factor = fmaf(fmaf(-f, t, 7.9375f), r, f);
     return s;
 }
 
 // Steps of 8 numbers.  y f + 1.5 2^23 has rint(y f) in its low bits (|y f| <= 127 and a
-// rounding): one fma in place of a product and a conversion, which has a quarter of the rate.
+// rounding): a sum in place of a conversion, which has a quarter of the rate.  The product is
+// rounded first: of a row's bf16 numbers many are half the largest, 63.5 steps, and the
+// rounding puts the product back on that tie where f is a little off.
 template <bool VEC>
 __device__ __forceinline__ void store_steps8(int8_t *row, int i, int width, const float (&y)[8], float f, bool on8) {
     uint32_t b[8];
@@ -175,7 +180,7 @@ __device__ __forceinline__ void store_steps8(int8_t *row, int i, int width, cons
 #pragma unroll
     for (int e = 0; e < 8; e += 2) {
         float lo, hi;
-        unpack(fma2(pack(y[e], y[e + 1]), ff, magic), &lo, &hi);
+        unpack(add2(mul2(pack(y[e], y[e + 1]), ff), magic), &lo, &hi);
         b[e] = __float_as_uint(lo);
         b[e + 1] = __float_as_uint(hi);
     }
