@@ -247,21 +247,25 @@ __device__ __forceinline__ void store_few(float *p, const float (&x)[N]) {
 // [2^-64, 2^64] within four tokens ends the four early.
 //
 // The warps bring the tokens after next into shared memory, as fp32 and normalised,
-// and form the next four's dot products, beside the present four.  A group's rows
+// and form the next ones' dot products, beside the present ones.  A group's rows
 // are interleaved, so that the groups' 16-byte reads of k and q meet in no bank.
-template <int R, bool BF16, int W>
-__global__ void __launch_bounds__(W * 32, R == 16 ? 12 / W : 1) recurrent_ragged_kernel(const PoolParams p) {
+// LONG: two fours between barriers, twice the registers, and the longest sequences
+// first.  48 sequences of 0 to 600 tokens (5155 in all), 32 heads of 128 x 128: 650 us;
+// the fma's alone would take 225 (an f32x2 takes two cycles of its pipe).
+template <int R, bool BF16, int W, bool LONG>
+__global__ void __launch_bounds__(W * 32, R < 16 ? 1 : LONG ? 8 / W : 12 / W) recurrent_ragged_kernel(const PoolParams p) {
+    constexpr int kBring = LONG ? 2 * kFour : kFour; // tokens between two barriers
     constexpr int kDk = R * kGroups, kThreads = W * 32, kWide = W * kCols;
     constexpr int kRun = R < 4 ? R : 4;              // consecutive rows
-    constexpr int kMine = kFour / W;                 // tokens a warp brings
+    constexpr int kMine = kBring / W;                // tokens of those a warp brings
     constexpr int kPer = (kDk + 31) / 32, kPerV = kWide / 32;   // numbers of k, v a lane brings
-    constexpr int kDot = kThreads / 16;              // threads that share a dot product
-    __shared__ __align__(16) float ks[3][kFour][kDk], qs[3][kFour][kDk], vs[3][kFour][kWide];
-    __shared__ __align__(16) float alphas[3][kFour], betas[3][kFour], kk[2][kFour][kFour], kq[2][kFour][kFour];
+    constexpr int kDot = kThreads / (4 * kBring);    // threads that share a dot product
+    __shared__ __align__(16) float ks[3][kBring][kDk], qs[3][kBring][kDk], vs[3][kBring][kWide];
+    __shared__ __align__(16) float alphas[3][kBring], betas[3][kBring], kk[2][kBring][kFour], kq[2][kBring][kFour];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slices = p.dv / kWide;
     const int slice = blockIdx.x % slices, h = blockIdx.x / slices % p.H;
     int s = blockIdx.x / slices / p.H;
-    if (p.rows / 16 >= p.seqs) s = longest_first<kThreads>(p, s);
+    if (LONG) s = longest_first<kThreads>(p, s);
     int slot, begin, end;
     if (!sequence(p, s, &slot, &begin, &end)) return;
     if (slot < 0) {                      // no sequence: zero rows of o
@@ -276,7 +280,7 @@ __global__ void __launch_bounds__(W * 32, R == 16 ? 12 / W : 1) recurrent_ragged
     const int pitch = p.dv / 4;          // float4 a row
     F2 g[R / 2][4];
 
-    // this warp's tokens of a four, from memory (zeros behind the end): kPer consecutive
+    // this warp's tokens of a bring, from memory (zeros behind the end): kPer consecutive
     // numbers of q and k a lane, kPerV of v
     Raw<kPer, BF16> kr[kMine], qr[kMine];
     Raw<kPerV, BF16> vr[kMine];
@@ -287,7 +291,7 @@ __global__ void __launch_bounds__(W * 32, R == 16 ? 12 / W : 1) recurrent_ragged
     auto fetch = [&](int n) {
 #pragma unroll
         for (int m = 0; m < kMine; ++m) {
-            const int64_t t = (int64_t)begin + n * kFour + warp + m * W;
+            const int64_t t = (int64_t)begin + n * kBring + warp + m * W;
             kr[m].zero(); qr[m].zero(); vr[m].zero();
             ar[m] = br[m] = 1.f;
             if (t < end) {
@@ -335,22 +339,18 @@ __global__ void __launch_bounds__(W * 32, R == 16 ? 12 / W : 1) recurrent_ragged
             if (lane == 0) { alphas[b][i0] = ar[m]; betas[b][i0] = br[m]; }
         }
     };
-    // 6 products k_i . k_j (j < i) and 10 q_i . k_j (j <= i), kDot threads each
-    const int dot = threadIdx.x / kDot, part = threadIdx.x % kDot, de = dot < 6 ? dot : dot - 6;
-    const int dot_i0 = de < 1 ? 0 : de < 3 ? 1 : de < 6 ? 2 : 3, dot_j = de - dot_i0 * (dot_i0 + 1) / 2;
-    const int dot_i = dot < 6 ? dot_i0 + 1 : dot_i0;
+    // for each four of a bring, 6 products k_i . k_j (j < i) and 10 q_i . k_j (j <= i), kDot threads each
+    const int dot = threadIdx.x / kDot % 16, four = threadIdx.x / kDot / 16 * kFour, part = threadIdx.x % kDot;
+    const int de = dot < 6 ? dot : dot - 6, dot_i0 = de < 1 ? 0 : de < 3 ? 1 : de < 6 ? 2 : 3;
+    const int dot_j = de - dot_i0 * (dot_i0 + 1) / 2, dot_i = four + (dot < 6 ? dot_i0 + 1 : dot_i0);
     auto dots = [&](int b, int to) {
-        const float *x = dot < 6 ? ks[b][dot_i] : qs[b][dot_i], *y = ks[b][dot_j];
+        const float4 *x = reinterpret_cast<const float4 *>(dot < 6 ? ks[b][dot_i] : qs[b][dot_i]) + part;
+        const float4 *y = reinterpret_cast<const float4 *>(ks[b][four + dot_j]) + part;
         float sum = 0.f;
-        if constexpr (kDk >= 4 * kDot) {
 #pragma unroll
-            for (int m = 0; m < kDk / 4 / kDot; ++m) {
-                const float4 u = reinterpret_cast<const float4 *>(x)[part + m * kDot], v = reinterpret_cast<const float4 *>(y)[part + m * kDot];
-                sum = fmaf(u.x, v.x, fmaf(u.y, v.y, fmaf(u.z, v.z, fmaf(u.w, v.w, sum))));
-            }
-        } else {
-#pragma unroll
-            for (int m = 0; m < kDk / kDot; ++m) sum = fmaf(x[part + m * kDot], y[part + m * kDot], sum);
+        for (int m = 0; m < kDk / 4 / kDot; ++m) {
+            const float4 u = x[m * kDot], v = y[m * kDot];
+            sum = fmaf(u.x, v.x, fmaf(u.y, v.y, fmaf(u.z, v.z, fmaf(u.w, v.w, sum))));
         }
 #pragma unroll
         for (int m = 1; m < kDot; m *= 2) sum = xor_add(sum, m);
@@ -395,17 +395,18 @@ __global__ void __launch_bounds__(W * 32, R == 16 ? 12 / W : 1) recurrent_ragged
     int64_t oi = ((int64_t)begin * p.H + h) * p.dv + slice * kWide + mine;
     float A = 1.f;
 
-    // `cnt` tokens from token i0 of the four in buffer b, with products in buffer d;
-    // Ai: the decays up to each of them.  ALL: cnt = 4, i0 = 0.
-    auto advance = [&](auto all, int b, int d, int i0, int cnt, const float (&Ai)[kFour]) {
+    // `cnt` tokens from token i0 of the four that starts at token f of the bring in buffer b,
+    // with products in buffer d; Ai: the decays up to each of them.  ALL: cnt = 4, i0 = 0.
+    auto advance = [&](auto all, int b, int d, int f, int i0, int cnt, const float (&Ai)[kFour]) {
         constexpr bool ALL = decltype(all)::value;
         if (ALL) i0 = 0;
+        const int at = f + i0;
         auto has = [&](int i) { return ALL || i < cnt; };
         float sum[kFour], u[kFour];      // P in the lanes with bit 2 clear, Q in those with it set
 #pragma unroll
         for (int i = 0; i < kFour; ++i) {
             float P[4] = {0.f, 0.f, 0.f, 0.f}, Q[4] = {0.f, 0.f, 0.f, 0.f};
-            if (has(i)) { partial(ks[b][i0 + i], P); partial(qs[b][i0 + i], Q); }
+            if (has(i)) { partial(ks[b][at + i], P); partial(qs[b][at + i], Q); }
             const float x = halve(P), y = halve(Q);
             sum[i] = (is_q ? y : x) + __shfl_xor_sync(~0u, is_q ? x : y, 4);
         }
@@ -415,8 +416,8 @@ __global__ void __launch_bounds__(W * 32, R == 16 ? 12 / W : 1) recurrent_ragged
             float y = sum[i];
 #pragma unroll
             for (int j = 0; j < i; ++j)
-                if (has(i)) y = fmaf(kk[d][i0 + i][i0 + j], u[j], y);
-            u[i] = has(i) ? betas[b][i0 + i] * (__fdividef(vs[b][i0 + i][mine], Ai[i]) - y) : 0.f;
+                if (has(i)) y = fmaf(kk[d][at + i][i0 + j], u[j], y);
+            u[i] = has(i) ? betas[b][at + i] * (__fdividef(vs[b][at + i][mine], Ai[i]) - y) : 0.f;
         }
 #pragma unroll
         for (int i = 0; i < kFour; ++i) {
@@ -428,7 +429,7 @@ __global__ void __launch_bounds__(W * 32, R == 16 ? 12 / W : 1) recurrent_ragged
             if (has(i)) {
                 float y = sum[i];
 #pragma unroll
-                for (int j = 0; j <= i; ++j) y = fmaf(kq[d][i0 + i][i0 + j], u[j], y);
+                for (int j = 0; j <= i; ++j) y = fmaf(kq[d][at + i][i0 + j], u[j], y);
                 if (is_q) store_o(p, oi, Ai[i] * y);
                 oi += o_row;
             }
@@ -440,7 +441,7 @@ __global__ void __launch_bounds__(W * 32, R == 16 ? 12 / W : 1) recurrent_ragged
             const float y[4] = {hi ? w0 : u0, hi ? w1 : u1, hi ? u0 : w0, hi ? u1 : w1};
             if (has(i)) {
                 F2 kp[R / 2];
-                rows_at(ks[b][i0 + i], kp);
+                rows_at(ks[b][at + i], kp);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     const F2 uu = pack(y[c], y[c]);
@@ -459,14 +460,14 @@ __global__ void __launch_bounds__(W * 32, R == 16 ? 12 / W : 1) recurrent_ragged
             for (int c = 0; c < 4; ++c) g[r][c] = mul2(g[r][c], f);
     };
 
-    const int fours = (end - begin + kFour - 1) / kFour;
+    const int brings = (end - begin + kBring - 1) / kBring;
     fetch(0);                            // before the state: it is needed first
     float4 rows[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) rows[r] = __ldcg(hp + row_of(r) * pitch);
     keep(0);
-    if (fours > 1) { fetch(1); keep(1); }
-    if (fours > 2) fetch(2);
+    if (brings > 1) { fetch(1); keep(1); }
+    if (brings > 2) fetch(2);
 #pragma unroll
     for (int r = 0; r < R; r += 2) {
         g[r / 2][0] = pack(rows[r].x, rows[r + 1].x); g[r / 2][1] = pack(rows[r].y, rows[r + 1].y);
@@ -476,38 +477,41 @@ __global__ void __launch_bounds__(W * 32, R == 16 ? 12 / W : 1) recurrent_ragged
     dots(0, 0);
     __syncthreads();
     int b = 0;                           // n % 3
-    for (int n = 0; n < fours; ++n) {
+    for (int n = 0; n < brings; ++n) {
         const int next = b == 2 ? 0 : b + 1, after = next == 2 ? 0 : next + 1;
-        // four n + 2, fetched one four ago, takes the place of four n - 1
-        if (n + 2 < fours) keep(after);
-        if (n + 3 < fours) fetch(n + 3);
-        const int tokens = min(kFour, end - begin - n * kFour);
-        constexpr float kLo = 2.3283064e-10f, kHi = 4.2949673e9f, kLo2 = 5.4210109e-20f, kHi2 = 1.8446744e19f;   // 2^-+32, 2^-+64
-        float Ai[kFour];
-        Ai[0] = A * alphas[b][0];
+        // bring n + 2, fetched one bring ago, takes the place of bring n - 1
+        if (n + 2 < brings) keep(after);
+        if (n + 3 < brings) fetch(n + 3);
+#pragma unroll 1
+        for (int f = 0; f < kBring; f += kFour) {
+            const int tokens = min(kFour, end - begin - n * kBring - f);
+            if (tokens <= 0) break;
+            constexpr float kLo = 2.3283064e-10f, kHi = 4.2949673e9f, kLo2 = 5.4210109e-20f, kHi2 = 1.8446744e19f;   // 2^-+32, 2^-+64
+            const float4 al = *reinterpret_cast<const float4 *>(&alphas[b][f]);
+            float Ai[kFour];
+            Ai[0] = A * al.x; Ai[1] = Ai[0] * al.y; Ai[2] = Ai[1] * al.z; Ai[3] = Ai[2] * al.w;
+            if (tokens == kFour && in(Ai[0], kLo, kHi) && in(Ai[1], kLo2, kHi2) && in(Ai[2], kLo2, kHi2) && in(Ai[3], kLo2, kHi2)) {
+                advance(std::true_type(), b, n & 1, f, 0, kFour, Ai);
+                A = Ai[3];
+            } else {
+                for (int i0 = 0, cnt; i0 < tokens; i0 += cnt) {
+                    Ai[0] = A * alphas[b][f + i0];
+                    if (!in(Ai[0], kLo, kHi)) { into_g(Ai[0]); Ai[0] = 1.f; }
+                    A = Ai[0];
+                    cnt = 1;
 #pragma unroll
-        for (int i = 1; i < kFour; ++i) Ai[i] = Ai[i - 1] * alphas[b][i];
-        if (tokens == kFour && in(Ai[0], kLo, kHi) && in(Ai[1], kLo2, kHi2) && in(Ai[2], kLo2, kHi2) && in(Ai[3], kLo2, kHi2)) {
-            advance(std::true_type(), b, n & 1, 0, kFour, Ai);
-            A = Ai[3];
-        } else {
-            for (int i0 = 0, cnt; i0 < tokens; i0 += cnt) {
-                Ai[0] = A * alphas[b][i0];
-                if (!in(Ai[0], kLo, kHi)) { into_g(Ai[0]); Ai[0] = 1.f; }
-                A = Ai[0];
-                cnt = 1;
-#pragma unroll
-                for (int i = 1; i < kFour; ++i) {
-                    Ai[i] = 1.f;
-                    if (cnt == i && i0 + i < tokens) {
-                        const float x = Ai[i - 1] * alphas[b][i0 + i];
-                        if (in(x, kLo2, kHi2)) { Ai[i] = A = x; cnt = i + 1; }
+                    for (int i = 1; i < kFour; ++i) {
+                        Ai[i] = 1.f;
+                        if (cnt == i && i0 + i < tokens) {
+                            const float x = Ai[i - 1] * alphas[b][f + i0 + i];
+                            if (in(x, kLo2, kHi2)) { Ai[i] = A = x; cnt = i + 1; }
+                        }
                     }
+                    advance(std::false_type(), b, n & 1, f, i0, cnt, Ai);
                 }
-                advance(std::false_type(), b, n & 1, i0, cnt, Ai);
             }
         }
-        if (n + 1 < fours) dots(next, (n + 1) & 1);
+        if (n + 1 < brings) dots(next, (n + 1) & 1);
         __syncthreads();
         b = next;
     }
@@ -521,12 +525,20 @@ __global__ void __launch_bounds__(W * 32, R == 16 ? 12 / W : 1) recurrent_ragged
     }
 }
 
+template <int R, bool BF16, int W>
+void launch_ragged(const PoolParams &p, bool is_long, unsigned blocks, cudaStream_t stream) {
+    if (is_long) recurrent_ragged_kernel<R, BF16, W, true><<<blocks, W * 32, 0, stream>>>(p);
+    else recurrent_ragged_kernel<R, BF16, W, false><<<blocks, W * 32, 0, stream>>>(p);
+}
 template <int R, bool BF16>
 void launch_r(const PoolParams &p, cudaStream_t stream) {
     unsigned blocks = (unsigned)p.seqs * (unsigned)p.H;
     if (p.cu_seqlens) {
-        if (p.dv % 64 == 0) recurrent_ragged_kernel<R, BF16, 4><<<blocks * (p.dv / 64), 128, 0, stream>>>(p);
-        else recurrent_ragged_kernel<R, BF16, 2><<<blocks * (p.dv / 32), 64, 0, stream>>>(p);
+        // LONG where sequences have 16 tokens and more on average: 600 tokens of 16 heads 213 us
+        // (288 the other way); decode steps of 256 x 16 heads 106 us (131).
+        const bool is_long = p.rows / 16 >= p.seqs;
+        if (p.dv % 64 == 0) launch_ragged<R, BF16, 4>(p, is_long, blocks * (p.dv / 64), stream);
+        else launch_ragged<R, BF16, 2>(p, is_long, blocks * (p.dv / 32), stream);
     } else {
         // 64 columns a block (256 x 16 heads of 128 x 128: 86 us; 128 columns 90, 32 columns 90);
         // where the heads are fewer than two a SM, 32, so that more SMs take part (16 heads: 2.8 us,

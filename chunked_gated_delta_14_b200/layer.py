@@ -192,63 +192,89 @@ def recurrent_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, alpha: Opti
     if stream is not None:
         return _other_stream(stream, q.device, (q, k, v, alpha, beta, state, slots, cu_seqlens, out), lambda: recurrent_fwd(
             q, k, v, alpha, beta, state, slots, cu_seqlens, qk_norm_eps=qk_norm_eps, o_dtype=o_dtype, out=out))
+    # What a correct call looks like, tested in place (the tests are most of what a small call
+    # costs); _recurrent_refuse says what is wrong with another.
+    try:
+        N, Hk, dk = shape = q.shape
+        _, H, dv = v.shape
+        io, i, S = q.dtype, q.get_device(), N
+        P, gates = state.shape[0], (N, H)
+        qr, qh, q1 = q.stride()
+        kr, kh, k1 = k.stride()
+        vr, vh, v1 = v.stride()
+        ap = bp = ar = br = cp = sp = 0
+        fits = (i >= 0 and k.shape == shape and v.shape == (N, H, dv) and k.dtype is io and v.dtype is io and q1 == k1 == v1 == 1
+                and k.get_device() == i and v.get_device() == i and state.dtype is torch.float32 and state.get_device() == i
+                and state.shape == (P, H, dk, dv) and state.is_contiguous())
+        if alpha is not None:
+            ar, a1 = alpha.stride()
+            ap = alpha.data_ptr()
+            fits = fits and a1 == 1 and alpha.shape == gates and alpha.dtype is torch.float32 and alpha.get_device() == i
+        if beta is not None:
+            br, b1 = beta.stride()
+            bp = beta.data_ptr()
+            fits = fits and b1 == 1 and beta.shape == gates and beta.dtype is torch.float32 and beta.get_device() == i
+        if cu_seqlens is not None:
+            S = cu_seqlens.shape[0] - 1
+            cp = cu_seqlens.data_ptr()
+            fits = fits and S >= 0 and cu_seqlens.dtype is torch.int32 and cu_seqlens.stride() == (1,) and cu_seqlens.get_device() == i
+        if slots is not None:
+            sp = slots.data_ptr()
+            fits = fits and slots.shape == (S,) and slots.dtype is torch.int32 and slots.stride() == (1,) and slots.get_device() == i
+        if out is not None:
+            od = out.dtype
+            fits = fits and out.shape == (N, H, dv) and (o_dtype is None or od is o_dtype) and out.get_device() == i and out.is_contiguous()
+        else:
+            od = o_dtype or io
+        if torch.is_grad_enabled():
+            fits = fits and not any(t is not None and t.requires_grad for t in (q, k, v, alpha, beta, state, out))
+        fits = fits and io in _DTYPES and od in _DTYPES
+    except (AttributeError, TypeError, ValueError, IndexError):
+        fits = False
+    if not fits:
+        _recurrent_refuse(q, k, v, alpha, beta, state, slots, cu_seqlens, o_dtype, out)
+    if out is None:
+        dev = q.device
+        out = _empty((N, H, dv), (H * dv, dv, 1), device=dev, dtype=od) if cu_seqlens is None else torch.zeros((N, H, dv), device=dev, dtype=od)
+    _launch("gdn_recurrent_fwd", _pack_recurrent(
+        N, S, H, Hk, dk, dv, P, _DTYPES[io], _DTYPES[od], 0 if qk_norm_eps is None else 1, qk_norm_eps or 0.0,
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), qr, qh, kr, kh, vr, vh, ap, bp, ar, br, cp, sp, state.data_ptr(),
+        out.data_ptr()), i)
+    return out
+
+
+def _recurrent_refuse(q, k, v, alpha, beta, state, slots, cu_seqlens, o_dtype, out):
+    """Raises for what recurrent_fwd does not take; returns where only its quick test was too
+    strict (a dimension of one element with some other stride)."""
     _tensors(q=q, k=k, v=v, state=state)
     if q.dim() != 3 or v.dim() != 3 or state.dim() != 4:
         raise ValueError("q must be [N, Hk, dk], v [N, H, dv] and state [P, H, dk, dv]")
-    io, i, grad = q.dtype, q.get_device(), torch.is_grad_enabled()
-    N, Hk, dk = q.shape
-    _, H, dv = v.shape
-    P = state.shape[0]
-    S, dev = N, q.device
+    _first(q, "q", 3, _IO)
+    dev, (N, _, dk), (_, H, dv), S = q.device, q.shape, v.shape, q.shape[0]
+    _check(k, "k", q.shape, (q.dtype,), dev)
+    _check(v, "v", (N, H, dv), (q.dtype,), dev)
+    _check(state, "state", (state.shape[0], H, dk, dv), _F32, dev)
+    if alpha is not None:
+        _check(alpha, "alpha", (N, H), _F32, dev)
+    if beta is not None:
+        _check(beta, "beta", (N, H), _F32, dev)
     if cu_seqlens is not None:
         _tensors(cu_seqlens=cu_seqlens)
         if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
             raise ValueError("cu_seqlens must be [S + 1]")
         S = cu_seqlens.shape[0] - 1
-        if not _fits(cu_seqlens, (S + 1,), torch.int32, i, grad) or cu_seqlens.stride()[0] != 1:
-            _check(cu_seqlens, "cu_seqlens", (S + 1,), _I32, dev)
-    (qr, qh, q1), (kr, kh, k1), (vr, vh, v1) = q.stride(), k.stride(), v.stride()
-    if not (i >= 0 and io in _DTYPES and _fits(q, q.shape, io, i, grad) and _fits(k, q.shape, io, i, grad) and _fits(v, (N, H, dv), io, i, grad)
-            and q1 == k1 == v1 == 1):
-        _first(q, "q", 3, _IO)
-        _check(k, "k", q.shape, (io,), dev)
-        _check(v, "v", (N, H, dv), (io,), dev)
-    if not _fits(state, (P, H, dk, dv), torch.float32, i, grad):
-        _check(state, "state", (P, H, dk, dv), _F32, dev)
+        _check(cu_seqlens, "cu_seqlens", (S + 1,), _I32, dev)
+    if slots is not None:
+        _check(slots, "slots", (S,), _I32, dev)
     if not state.is_contiguous():
         raise ValueError("state must be contiguous")
-    ap = bp = ar = br = cp = sp = 0
-    if alpha is not None:
-        _tensors(alpha=alpha)
-        if not _fits(alpha, (N, H), torch.float32, i, grad) or alpha.stride()[1] != 1:
-            _check(alpha, "alpha", (N, H), _F32, dev)
-        ap, ar = alpha.data_ptr(), alpha.stride()[0]
-    if beta is not None:
-        _tensors(beta=beta)
-        if not _fits(beta, (N, H), torch.float32, i, grad) or beta.stride()[1] != 1:
-            _check(beta, "beta", (N, H), _F32, dev)
-        bp, br = beta.data_ptr(), beta.stride()[0]
-    if slots is not None:
-        _tensors(slots=slots)
-        if not _fits(slots, (S,), torch.int32, i, grad) or slots.stride()[0] != 1:
-            _check(slots, "slots", (S,), _I32, dev)
-        sp = slots.data_ptr()
-    if cu_seqlens is not None:
-        cp = cu_seqlens.data_ptr()
-    if out is None:
-        make = torch.empty if cu_seqlens is None else torch.zeros
-        out = make((N, H, dv), device=dev, dtype=o_dtype or io)
-    else:
+    _code(q.dtype), _code(o_dtype or q.dtype)
+    if out is not None:
         _tensors(out=out)
-        if not _fits(out, (N, H, dv), o_dtype or out.dtype, i, grad):
-            _check(out, "out", (N, H, dv), (o_dtype or out.dtype,), dev)
+        _check(out, "out", (N, H, dv), (o_dtype or out.dtype,), dev)
+        _code(out.dtype)
         if not out.is_contiguous():
             raise ValueError("out must be contiguous")
-    _launch("gdn_recurrent_fwd", _pack_recurrent(
-        N, S, H, Hk, dk, dv, P, _DTYPES[io], _code(out.dtype), 0 if qk_norm_eps is None else 1, qk_norm_eps or 0.0,
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), qr, qh, kr, kh, vr, vh, ap, bp, ar, br, cp, sp, state.data_ptr(),
-        out.data_ptr()), i)
-    return out
 
 
 def _tensors(**named):
