@@ -77,7 +77,7 @@ def _check(t, name, shape, dtypes, device):
         raise TypeError(f"{name} has dtype {t.dtype}, expected " + " or ".join(map(str, dtypes)))
     if t.requires_grad and torch.is_grad_enabled():
         raise ValueError(f"{name} requires a gradient: the decode-layer operators have none")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+    if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
 
 
@@ -114,9 +114,11 @@ def _rows(t, name):
     return t.shape[0], t.stride(0)
 
 
-def _other_stream(stream, device, tensors, call):
+def _other_stream(stream, first, tensors, call):
     """``call()`` on ``stream``: what it allocates belongs to that stream, and what it
     reads or writes stays allocated until the stream is past it."""
+    _first(first, "the first tensor", 0, (first.dtype,) if isinstance(first, torch.Tensor) else ())
+    device = first.device
     if stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
     with torch.cuda.stream(stream):
@@ -190,7 +192,7 @@ def recurrent_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, alpha: Opti
     of hundreds of tokens run quicker through ``chunk_fwd``.
     """
     if stream is not None:
-        return _other_stream(stream, q.device, (q, k, v, alpha, beta, state, slots, cu_seqlens, out), lambda: recurrent_fwd(
+        return _other_stream(stream, q, (q, k, v, alpha, beta, state, slots, cu_seqlens, out), lambda: recurrent_fwd(
             q, k, v, alpha, beta, state, slots, cu_seqlens, qk_norm_eps=qk_norm_eps, o_dtype=o_dtype, out=out))
     # What a correct call looks like, tested in place (the tests are most of what a small call
     # costs); _recurrent_refuse says what is wrong with another.
@@ -312,7 +314,7 @@ def add_rms_norm_int8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, re
     (which may be ``residual``), None without a residual.  The norm takes h before that
     rounding.  Rows of zeros have scale 0, rows with an infinity or a NaN scale NaN."""
     if stream is not None:
-        return _other_stream(stream, x.device, (x, weight, residual, residual_out), lambda: add_rms_norm_int8(
+        return _other_stream(stream, x, (x, weight, residual, residual_out), lambda: add_rms_norm_int8(
             x, weight, residual, eps=eps, residual_out=residual_out))
     i, grad, xd = _row_input(x, 1)
     shape, dev = x.shape, x.device
@@ -381,7 +383,7 @@ def gated_rms_norm_int8(x: torch.Tensor, gate: torch.Tensor, weight: Optional[to
     stride), d a multiple of 8 up to 256; weight: [d] (bf16 or fp32; None = 1).  q: [..., H * d]
     int8, its rows on 16-byte boundaries; scale: [...] fp32, one for all heads of a row."""
     if stream is not None:
-        return _other_stream(stream, x.device, (x, gate, weight), lambda: gated_rms_norm_int8(x, gate, weight, eps=eps))
+        return _other_stream(stream, x, (x, gate, weight), lambda: gated_rms_norm_int8(x, gate, weight, eps=eps))
     i, grad, xd = _row_input(x, 2)
     dev = x.device
     *lead, H, d = x.shape
@@ -404,7 +406,7 @@ def quantize_int8(x: torch.Tensor, *, stream: Optional[torch.cuda.Stream] = None
     weight [N, K] for ``int8_matmul``.  q: [..., D] int8, its rows on 16-byte boundaries
     whatever D is; scale: [...] fp32, the row's largest absolute value / 127."""
     if stream is not None:
-        return _other_stream(stream, x.device, (x,), lambda: quantize_int8(x))
+        return _other_stream(stream, x, (x,), lambda: quantize_int8(x))
     i, _, xd = _row_input(x, 1)
     D = x.shape[-1]
     rows, xr = _rows(x, "x")
@@ -424,7 +426,7 @@ def int8_matmul(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale
     lay them out) are read where they are; others are copied to such rows first, in every
     call.  ``out``: [..., N] in ``out_dtype`` (bf16 or fp32), or None to allocate it."""
     if stream is not None:
-        return _other_stream(stream, x.device, (x, x_scale, w, w_scale, bias, out), lambda: int8_matmul(
+        return _other_stream(stream, x, (x, x_scale, w, w_scale, bias, out), lambda: int8_matmul(
             x, x_scale, w, w_scale, bias, out_dtype=out_dtype, out=out))
     _tensors(x=x, x_scale=x_scale, w=w, w_scale=w_scale)
     if w.dim() != 2:

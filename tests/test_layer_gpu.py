@@ -106,6 +106,41 @@ def test_recurrent_one_token_each(io, dk, dv, Hk, H):
     check_rule(o, state, want, range(S), starts, q, dk, 1)
 
 
+@pytest.mark.parametrize("io", [BF, F])
+@pytest.mark.parametrize("dk,dv,Hk,H", [(128, 128, 4, 8), (64, 96, 2, 4), (16, 64, 3, 9), (32, 32, 4, 4)])
+def test_recurrent_one_token_each_of_many_heads(io, dk, dv, Hk, H):
+    """Two blocks a SM and more, where a block takes more columns; some entries idle."""
+    S = 320 // H + 1
+    q, k, v, al, be, state, starts = make_rule(41, [1] * S, Hk, H, dk, dv, io, pool=S + 3, packed=True)
+    slots = torch.randperm(S + 3, generator=torch.Generator().manual_seed(1))[:S].tolist()
+    slots[5] = slots[S - 1] = -1
+    want = rule64(q, k, v, al, be, state, slots, starts, torch.zeros(S, H, dv, device="cuda"), 1e-6)
+    o = gdn.recurrent_fwd(q, k, v, al, be, state, torch.tensor(slots, dtype=torch.int32, device="cuda"), qk_norm_eps=1e-6, o_dtype=F)
+    gdn.device_check()
+    check_rule(o, state, want, slots, starts, q, dk, 1, 1e-6)
+    assert (o[5] == 0).all() and (o[S - 1] == 0).all()
+
+
+@pytest.mark.parametrize("lens", [[3, 2, 0, 1], [40, 30, 0, 20]])
+def test_recurrent_reads_nothing_of_idle_entries_and_rows_of_no_sequence(lens):
+    """NaN in the tokens and states that belong to no sequence."""
+    q, k, v, al, be, state, starts = make_rule(42, lens, 1, 2, 64, 64, BF, pool=6, tail=3)
+    slots = [4, -1, 0, 2]
+    cu = torch.tensor(starts, dtype=torch.int32, device="cuda")
+    want = rule64(q, k, v, al, be, state, slots, starts, torch.zeros(v.shape, device="cuda"))
+    for t in (q, k, v, al, be):
+        t[starts[1]:starts[2]] = math.nan
+        t[starts[4]:] = math.inf
+    for i in (1, 3, 5):
+        state[i] = math.nan
+    o = gdn.recurrent_fwd(q, k, v, al, be, state, torch.tensor(slots, dtype=torch.int32, device="cuda"), cu, o_dtype=F)
+    live = torch.tensor([0, 2, 4], device="cuda")
+    q[starts[1]:starts[2]] = 0
+    check_rule(o, state[live], (want[0], want[1][live], want[2][live]), [2, -1, 0, 1], starts, q, 64, max(lens))
+    assert (o[starts[1]:starts[2]] == 0).all() and (o[starts[4]:] == 0).all()
+    assert state[[1, 3, 5]].isnan().all()
+
+
 @pytest.mark.parametrize("io,packed,unit,o_dtype", [(BF, True, True, F), (BF, False, False, BF), (F, True, False, BF), (F, False, True, F)])
 @pytest.mark.parametrize("dk,dv,Hk,H", [(128, 128, 1, 4), (16, 96, 2, 2), (64, 32, 2, 6)])
 def test_recurrent_ragged_pool(io, packed, unit, o_dtype, dk, dv, Hk, H):
@@ -533,3 +568,75 @@ def test_the_same_call_twice_gives_the_same_bits():
     x, xs, w, ws, bias = make_product(35, 20, 600, 4096)
     one = gdn.int8_matmul(x, xs, w, ws, out_dtype=F)
     assert all(torch.equal(one, gdn.int8_matmul(x, xs, w, ws, out_dtype=F)) for _ in range(3))
+
+
+def test_product_with_copies_captured_twice():
+    """Two graphs of one stream, each with copies of unaligned rows: they share no workspace."""
+    a, b = make_product(36, 30, 70, 333, pad=False), make_product(37, 50, 90, 555, pad=False)
+    want = [gdn.int8_matmul(*t[:4], out_dtype=F) for t in (a, b)]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for t in (a, b):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(gdn.int8_matmul(*t[:4], out_dtype=F))
+        graphs.append(g)
+    s = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(5):
+        for g, st in zip(graphs, s):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(outs, want))
+
+
+def test_calls_from_threads_on_their_own_streams():
+    import threading
+    P, g = make_layer()
+    hidden, residual, start = randn(g, 6, 512).to(BF), randn(g, 6, 512), 0.05 * randn(g, 6, 4, 128, 128)
+    s0 = start.clone()
+    want = [layer(hidden, residual, P, s0, None, None) for _ in range(4)]
+    torch.cuda.synchronize()
+    errors = []
+
+    def work():
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                state = start.clone()
+                for o, r in want:
+                    got = layer(hidden, residual, P, state, None, None)
+                    assert torch.equal(got[0], o) and torch.equal(got[1], r)
+                assert torch.equal(state, s0)
+        except BaseException as e:      # noqa: B902 - handed to the test's own thread
+            errors.append(e)
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    gdn.device_check()
+    assert not errors, errors
+
+
+def test_recurrent_gives_the_same_bits_alone_and_in_a_batch():
+    """A sequence's result does not depend on its neighbours or its place."""
+    lens = [5, 9, 1, 4]
+    q, k, v, al, be, state, starts = make_rule(43, lens, 2, 4, 128, 128, BF)
+    s0 = state.clone()
+    o = gdn.recurrent_fwd(q, k, v, al, be, s0, None, torch.tensor(starts, dtype=torch.int32, device="cuda"))
+    for i in range(4):
+        a, e = starts[i], starts[i + 1]
+        s1 = state[i:i + 1].clone()
+        o1 = gdn.recurrent_fwd(q[a:e], k[a:e], v[a:e], al[a:e], be[a:e], s1, None, torch.tensor([0, e - a], dtype=torch.int32, device="cuda"))
+        assert torch.equal(o1, o[a:e]) and torch.equal(s1[0], s0[i])
+
+
+def test_nothing_is_recorded_for_gradients_and_leaves_are_refused():
+    x = randn(rng(44), 4, 64).requires_grad_()
+    with pytest.raises(ValueError, match="gradient"):
+        gdn.quantize_int8(x)
+    with torch.no_grad():
+        q, scale = gdn.quantize_int8(x)
+        w = torch.nn.Parameter(torch.ones(64, device="cuda"))
+        gdn.add_rms_norm_int8(x, w, x)
+    assert not scale.requires_grad
