@@ -8,10 +8,12 @@ WY products, state passing, output).  Inputs are synthetic (seeded), resident
 in HBM when the timed region starts.
 
   python bench.py [--gpus N --steps K --warmup W] [--impl reference] [--batch B]
-                  [--mode exact|neumann|residual] [--decode] [--bwd]
+                  [--mode exact|neumann|residual] [--decode [--layer]] [--bwd]
 
 ``--batch B`` replaces the batch size (a smaller case for profiler captures).
-``--decode`` times one-token decode steps; ``--bwd`` times the backward pass
+``--decode`` times one-token decode steps, ``--decode --layer`` those of a whole
+quantised layer (norm, projections in 8 bits, the rule, gated norm, projection);
+``--bwd`` times the backward pass
 (gradients of q, k, v, alpha, beta) on the same workload.  The default line
 also carries a short backward timing in its ``backward`` object
 (``--bwd-steps``, 0 to skip).
@@ -733,6 +735,134 @@ def run_decode(args, rank, world, local_rank):
         print(json.dumps(line), flush=True)
 
 
+LAYER_METRIC = "quantised-layer decode tokens/s (8-bit projections, bf16 activations, H=16, d=128, width 2048) and % of HBM roofline on 1 B200"
+
+
+def layer_weights(H, d, width, dev, seed):
+    """Random-init weights of a Gated DeltaNet layer, the projections' in 8 bits."""
+    import torch
+    import chunked_gated_delta_14_b200 as gdn
+    g = torch.Generator(dev).manual_seed(seed)
+    normal = lambda *s: torch.randn(*s, device=dev, generator=g)
+    rows_in = 4 * H * d + 2 * H              # q, k, v, gate; a decay and a strength for each head
+    return dict(H=H, d=d, norm=1 + 0.1 * normal(width), head=1 + 0.1 * normal(d),
+                w_in=gdn.quantize_int8((normal(rows_in, width) / width ** 0.5).to(torch.bfloat16)),
+                w_out=gdn.quantize_int8((normal(width, H * d) / (H * d) ** 0.5).to(torch.bfloat16)))
+
+
+def layer_step(p, hidden, residual, state, slots=None, cu_seqlens=None):
+    """One pass of the layer over tokens [N, width]: (its output, the residual stream).
+    residual and the states of the pool are updated in place."""
+    import torch
+    import chunked_gated_delta_14_b200 as gdn
+    H, d = p["H"], p["d"]
+    x, x_scale, residual = gdn.add_rms_norm_int8(hidden, p["norm"], residual, residual_out=residual)
+    row = gdn.int8_matmul(x, x_scale, *p["w_in"])
+    q, k, v, gate, ab = row.split([H * d] * 4 + [2 * H], dim=1)
+    q, k, v, gate = (t.unflatten(1, (H, d)) for t in (q, k, v, gate))
+    alpha = torch.exp(-torch.nn.functional.softplus(ab[:, :H].float() - 4))     # close to 1, as trained
+    beta = torch.sigmoid(ab[:, H:].float())
+    o = gdn.recurrent_fwd(q, k, v, alpha, beta, state, slots, cu_seqlens, qk_norm_eps=1e-6)
+    y, y_scale = gdn.gated_rms_norm_int8(o, gate, p["head"])
+    return gdn.int8_matmul(y, y_scale, *p["w_out"]), residual
+
+
+def layer_bytes(B, H, d, width):
+    """Per step: the states read and written, both projections' weights, and the rows in and
+    out of the layer (hidden bf16 in and out, residual fp32 read and written)."""
+    return B * H * 2 * d * d * 4 + (4 * H * d + 2 * H + H * d) * width + B * width * (2 + 2 + 8)
+
+
+def run_decode_layer(args, rank, world, local_rank):
+    """Decode steps of the quantised layer, one token for each of B sequences: captured once
+    in a CUDA graph for ``value``, called from Python for the end-to-end number."""
+    import torch
+    import chunked_gated_delta_14_b200 as gdn
+
+    torch.cuda.set_device(local_rank)
+    dev = torch.device("cuda", local_rank)
+    B, H, d, width = args.batch or 256, 16, 128, 2048
+    p = layer_weights(H, d, width, dev, seed=rank)
+    g = torch.Generator(dev).manual_seed(1000 + rank)
+    hidden = torch.randn(B, width, device=dev, generator=g).to(torch.bfloat16)
+    residual = torch.zeros(B, width, device=dev)
+    state = 0.02 * torch.randn(B, H, d, d, device=dev, generator=g)
+    for _ in range(max(args.warmup, 3)):
+        out, _ = layer_step(p, hidden, residual, state)
+    gdn.device_check()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, _ = layer_step(p, hidden, residual, state)
+    stream = torch.cuda.current_stream(dev)
+    for _ in range(max(args.warmup, 3)):
+        graph.replay()
+    torch.cuda.synchronize()
+    clocks = ClockSampler(local_rank)
+    if rank == 0:
+        clocks.start()
+        time.sleep(1.0)
+    if world > 1:
+        import torch.distributed as dist
+        dist.barrier()
+    torch.cuda.synchronize()
+    e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    t_wall0 = time.time()
+    e0.record(stream)
+    for _ in range(args.steps):
+        graph.replay()
+    e1.record(stream)
+    torch.cuda.synchronize()
+    t_wall1 = time.time()
+    ms = max_over_ranks(e0.elapsed_time(e1), world, dev)
+    clocks.mark(t_wall0, t_wall1)
+    time.sleep(0.3)
+    clocks.stop()
+    ms_step = ms / args.steps
+
+    # end to end: this step's hidden rows from pinned host memory, the layer's output back
+    host = hidden.cpu().pin_memory()
+    out_host = torch.empty(out.shape, dtype=out.dtype, pin_memory=True)
+    h2d, d2h = host.numel() * host.element_size(), out_host.numel() * out_host.element_size()
+
+    def e2e_step():
+        hidden.copy_(host, non_blocking=True)
+        y, _ = layer_step(p, hidden, residual, state)
+        out_host.copy_(y, non_blocking=True)
+
+    for _ in range(3):
+        e2e_step()
+    torch.cuda.synchronize()
+    f0, f1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    n_e2e = max(1, args.e2e_steps * 10)
+    f0.record(stream)
+    for _ in range(n_e2e):
+        e2e_step()
+    f1.record(stream)
+    torch.cuda.synchronize()
+    ems = max_over_ranks(f0.elapsed_time(f1), world, dev)
+    e2e = dict(value=job_throughput(B, world, n_e2e, ems), unit=UNIT, h2d_bytes_per_step=int(h2d),
+               d2h_bytes_per_step=int(d2h), ms_per_step=ems / n_e2e)
+    if rank == 0:
+        pk = peaks()
+        bytes_step = layer_bytes(B, H, d, width)
+        achieved = bytes_step / (ms_step / 1e3) / 1e9
+        print(json.dumps(dict(
+            metric=LAYER_METRIC, value=job_throughput(B, world, args.steps, ms), unit=UNIT, n_gpus=world, steps=args.steps,
+            warmup=args.warmup, ms_per_step=ms_step, higher_is_better=True, scaling="weak", vs_baseline=None, dtype="int8",
+            compute="8-bit rows and weights with 32-bit integer sums in the projections; bf16 activations; fp32 norms and state",
+            data="synthetic (seeded; random-init weights of Gated DeltaNet layer shapes)",
+            config=dict(workload=f"layer decode: B={B} H={H} d={d} width={width}, one token per sequence, states in place",
+                        global_batch=B * world, seq_len=1, parallelism=f"independent batch per GPU x{world}",
+                        l2=f"no flush: states {B * H * d * d * 4 / 1e6:.0f} MB read and written per step > 126 MB L2",
+                        kernel="rows_kernel, int8_matmul_kernel, recurrent_step_kernel, gated_kernel, int8_matmul_kernel (one CUDA graph)"),
+            clocks=clocks.summary(), e2e=e2e, gpu_launches=5 * args.steps,
+            roofline=dict(bound="hbm", achieved=achieved, peak=pk["hbm_gbs"], unit="GB/s", frac=achieved / pk["hbm_gbs"],
+                          traffic=None, peak_source=pk["source"] + " (burst copy bandwidth)",
+                          algorithmic_bytes_per_step=bytes_step, roofline_ms=bytes_step / (pk["hbm_gbs"] * 1e9) * 1e3),
+            cpu_baseline=None)), flush=True)
+
+
 BWD_METRIC = "backward tokens/s (bf16 in, fp32 gradients, H=16, d=128, T=4096) and % of fp32 roofline on 1 B200"
 BWD_SOURCES = ("gdn_bwd.cu", "gdn_bwd_kernels.cuh", "gdn_bwd_params.cuh")
 
@@ -1062,6 +1192,8 @@ def main():
                          "(order --N), or the series with --S residual-correction terms")
     ap.add_argument("--decode", action="store_true",
                     help="decode steps (T = 1, state in place, B = 256 unless --batch)")
+    ap.add_argument("--layer", action="store_true",
+                    help="with --decode: steps of the whole quantised layer")
     ap.add_argument("--bwd", action="store_true",
                     help="the backward pass (gradients) on the same workload")
     ap.add_argument("--bwd-steps", type=int, default=20,
@@ -1091,7 +1223,9 @@ def main():
         dist.init_process_group("nccl", timeout=datetime.timedelta(seconds=120),
                                 device_id=torch.device("cuda", local_rank))
     try:
-        if args.decode:
+        if args.decode and args.layer:
+            run_decode_layer(args, rank, world, local_rank)
+        elif args.decode:
             run_decode(args, rank, world, local_rank)
         elif args.bwd:
             run_bwd(args, rank, world, local_rank)

@@ -92,13 +92,6 @@ def _first(t, name, dims, dtypes):
     _check(t, name, t.shape, dtypes, t.device)
 
 
-def _fits(t, shape, dtype, i, grad):
-    """Whether a tensor is what ``_check`` lets pass but for its strides, quickly (the checks are
-    most of what a small call costs); where it is not, ``_check`` says what is wrong, or lets it
-    pass.  ``grad``: whether gradients are recorded."""
-    return t.shape == shape and t.dtype is dtype and t.get_device() == i and not (grad and t.requires_grad)
-
-
 _IO = (torch.bfloat16, torch.float32)
 _F32, _I32, _I8 = (torch.float32,), (torch.int32,), (torch.int8,)
 
@@ -318,23 +311,31 @@ def add_rms_norm_int8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, re
             x, weight, residual, eps=eps, residual_out=residual_out))
     i, grad, xd = _row_input(x, 1)
     shape, dev = x.shape, x.device
+    flat = len(shape) == 2
+    rows, xr = (shape[0], x.stride()[0]) if flat else _rows(x, "x")
     D = shape[-1]
-    rows, xr = _rows(x, "x")
-    rr = ror = rdt = wdt = rp = wp = rop = 0
+    rr = ror = rdt = wdt = wp = rp = rop = 0
     if weight is not None:
         wdt, wp = _row_weight(weight, (D,), i, grad, dev)
     if residual is not None:
-        _tensors(residual=residual)
-        rd = residual.dtype
-        if not (rd in _DTYPES and _fits(residual, shape, rd, i, grad) and residual.stride()[-1] == 1):
+        try:
+            rd, (rr, r1) = residual.dtype, residual.stride()
+            fits = flat and r1 == 1 and residual.shape == shape and rd in _DTYPES and residual.get_device() == i and not (grad and residual.requires_grad)
+        except (AttributeError, ValueError):
+            fits = False
+        if not fits:
+            _tensors(residual=residual)
             _check(residual, "residual", shape, _IO, dev)
-        rdt, rp, rr = _DTYPES[rd], residual.data_ptr(), _rows(residual, "residual")[1]
+            rd, rr = residual.dtype, _rows(residual, "residual")[1]
+        rdt, rp = _DTYPES[rd], residual.data_ptr()
         if residual_out is None:
-            residual_out = _empty(shape, (D, 1), device=dev, dtype=rd) if len(shape) == 2 else torch.empty(shape, device=dev, dtype=rd)
+            residual_out = _empty(shape, (D, 1), device=dev, dtype=rd) if flat else torch.empty(shape, device=dev, dtype=rd)
+            ror = D
         else:
             _tensors(residual_out=residual_out)
             _check(residual_out, "residual_out", shape, (rd,), dev)
-        rop, ror = residual_out.data_ptr(), _rows(residual_out, "residual_out")[1]
+            ror = _rows(residual_out, "residual_out")[1]
+        rop = residual_out.data_ptr()
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
     q, qr, scale = _steps(shape[:-1], rows, D, dev)
@@ -345,19 +346,28 @@ def add_rms_norm_int8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, re
 
 def _row_input(x, dims):
     """(device index, whether gradients are recorded, dtype code) of a checked x."""
-    _tensors(x=x)
-    i, grad, xd = x.get_device(), torch.is_grad_enabled(), _DTYPES.get(x.dtype)
-    if xd is None or i < 0 or x.dim() < dims or (grad and x.requires_grad) or x.stride()[-1] != 1:
+    grad = torch.is_grad_enabled()
+    try:
+        i, xd, stride = x.get_device(), _DTYPES.get(x.dtype), x.stride()
+        fits = xd is not None and i >= 0 and len(stride) >= dims and stride[-1] == 1 and not (grad and x.requires_grad)
+    except AttributeError:
+        fits = False
+    if not fits:
         _first(x, "x", dims, _IO)
     return i, grad, xd
 
 
 def _row_weight(weight, shape, i, grad, dev):
-    _tensors(weight=weight)
-    wd = weight.dtype
-    if not (wd in _DTYPES and _fits(weight, shape, wd, i, grad) and weight.stride()[0] == 1):
+    try:
+        wd = weight.dtype
+        fits = (wd in _DTYPES and weight.shape == shape and weight.stride() == (1,) and weight.get_device() == i
+                and not (grad and weight.requires_grad))
+    except AttributeError:
+        fits = False
+    if not fits:
+        _tensors(weight=weight)
         _check(weight, "weight", shape, _IO, dev)
-    return _DTYPES[wd], weight.data_ptr()
+    return _DTYPES[weight.dtype], weight.data_ptr()
 
 
 def _head_rows(t, name):
@@ -386,10 +396,16 @@ def gated_rms_norm_int8(x: torch.Tensor, gate: torch.Tensor, weight: Optional[to
         return _other_stream(stream, x, (x, gate, weight), lambda: gated_rms_norm_int8(x, gate, weight, eps=eps))
     i, grad, xd = _row_input(x, 2)
     dev = x.device
-    *lead, H, d = x.shape
-    _tensors(gate=gate)
-    if not (_fits(gate, x.shape, x.dtype, i, grad) and gate.stride()[-1] == 1):
-        _check(gate, "gate", x.shape, (x.dtype,), dev)
+    shape = x.shape
+    *lead, H, d = shape
+    try:
+        fits = (gate.shape == shape and gate.dtype is x.dtype and gate.get_device() == i and gate.stride()[-1] == 1
+                and not (grad and gate.requires_grad))
+    except AttributeError:
+        fits = False
+    if not fits:
+        _tensors(gate=gate)
+        _check(gate, "gate", shape, (x.dtype,), dev)
     wdt = wp = 0
     if weight is not None:
         wdt, wp = _row_weight(weight, (d,), i, grad, dev)
@@ -428,23 +444,23 @@ def int8_matmul(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale
     if stream is not None:
         return _other_stream(stream, x, (x, x_scale, w, w_scale, bias, out), lambda: int8_matmul(
             x, x_scale, w, w_scale, bias, out_dtype=out_dtype, out=out))
-    _tensors(x=x, x_scale=x_scale, w=w, w_scale=w_scale)
-    if w.dim() != 2:
-        raise ValueError("w must be [N, K]")
-    (N, wk), shape, i, grad, dev = w.shape, x.shape, x.get_device(), torch.is_grad_enabled(), x.device
-    if i < 0 or not len(shape) or x.dtype is not torch.int8 or x.stride()[-1] != 1:
-        _first(x, "x", 1, _I8)
-    lead, K = shape[:-1], shape[-1]
-    if not (wk == K and _fits(w, (N, K), torch.int8, i, False) and w.stride()[1] == 1):
-        _check(w, "w", (N, K), _I8, dev)
-    if not (_fits(w_scale, (N,), torch.float32, i, grad) and w_scale.stride()[0] == 1):
-        _check(w_scale, "w_scale", (N,), _F32, dev)
-    if not (_fits(x_scale, lead, torch.float32, i, grad) and x_scale.is_contiguous()):
-        _check_scale(x_scale, lead, dev)
+    grad = torch.is_grad_enabled()
+    try:
+        shape, i = x.shape, x.get_device()
+        lead, K = shape[:-1], shape[-1]
+        N, wk = w.shape
+        wr, w1 = w.stride()
+        fits = (i >= 0 and x.dtype is torch.int8 and x.stride()[-1] == 1 and wk == K and w1 == 1 and w.dtype is torch.int8
+                and w.get_device() == i and w_scale.shape == (N,) and w_scale.dtype is torch.float32 and w_scale.stride() == (1,)
+                and w_scale.get_device() == i and x_scale.shape == lead and x_scale.dtype is torch.float32
+                and x_scale.get_device() == i and x_scale.is_contiguous() and not (grad and (x_scale.requires_grad or w_scale.requires_grad)))
+    except (AttributeError, TypeError, ValueError, IndexError):
+        fits = False
+    dev = x.device if fits else _product_refuse(x, x_scale, w, w_scale)
     bp = 0
     if bias is not None:
         _tensors(bias=bias)
-        if not (_fits(bias, (N,), torch.float32, i, grad) and bias.stride()[0] == 1):
+        if not (bias.shape == (N,) and bias.dtype is torch.float32 and bias.stride() == (1,) and bias.get_device() == i and not (grad and bias.requires_grad)):
             _check(bias, "bias", (N,), _F32, dev)
         bp = bias.data_ptr()
     M, xr = _rows(x, "x")
@@ -456,17 +472,30 @@ def int8_matmul(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale
         _tensors(out=out)
         _check(out, "out", (*lead, N), (out_dtype,), dev)
         outr = _rows(out, "out")[1]
-    wr, xp, wp = w.stride()[0], x.data_ptr(), w.data_ptr()
+    xp, wp = x.data_ptr(), w.data_ptr()
     fields = (M, N, K, od, xp, wp, xr, wr, outr, x_scale.data_ptr(), w_scale.data_ptr(), bp, out.data_ptr())
     ws = need = 0
     if (xp | wp | xr | wr) & 15 or not xr or not wr:
         # from torch's allocator and not kept: a call's copies belong to its stream, or its graph
         need = lib().gdn_int8_matmul_workspace_bytes(_pack_matmul(*fields, 0, 0))
         if need:
-            buffer = torch.empty(need, device=dev, dtype=torch.uint8)
+            buffer = _empty((need,), (1,), device=dev, dtype=torch.uint8)
             ws = buffer.data_ptr()
     _launch("gdn_int8_matmul", _pack_matmul(*fields, ws, need), i)
     return out
+
+
+def _product_refuse(x, x_scale, w, w_scale):
+    """Raises for what int8_matmul does not take; the device where only its quick test was too
+    strict."""
+    _tensors(x=x, x_scale=x_scale, w=w, w_scale=w_scale)
+    if w.dim() != 2:
+        raise ValueError("w must be [N, K]")
+    _first(x, "x", 1, _I8)
+    _check(w, "w", (w.shape[0], x.shape[-1]), _I8, x.device)
+    _check(w_scale, "w_scale", (w.shape[0],), _F32, x.device)
+    _check_scale(x_scale, x.shape[:-1], x.device)
+    return x.device
 
 
 def _check_scale(t, lead, dev):

@@ -8,6 +8,7 @@ import math
 import pytest
 import torch
 
+import bench
 import chunked_gated_delta_14_b200 as gdn
 
 pytestmark = pytest.mark.gpu
@@ -460,16 +461,7 @@ def test_product_of_rows_that_are_not_finite():
 # ------------------------------------------------------------------ together
 
 def layer(hidden, residual, P, state, slots, cu):
-    H, d = P["H"], P["d"]
-    xq, xs, residual = gdn.add_rms_norm_int8(hidden, P["norm"], residual)
-    row = gdn.int8_matmul(xq, xs, *P["in"])
-    q, k, v, gate, ab = row.split([H * d] * 4 + [2 * H], dim=1)
-    q, k, v, gate = (t.unflatten(1, (H, d)) for t in (q, k, v, gate))
-    alpha = torch.exp(-torch.nn.functional.softplus(ab[:, :H].float()))
-    beta = torch.sigmoid(ab[:, H:].float())
-    o = gdn.recurrent_fwd(q, k, v, alpha, beta, state, slots, cu, qk_norm_eps=1e-6)
-    oq, os_ = gdn.gated_rms_norm_int8(o, gate, P["head"])
-    return gdn.int8_matmul(oq, os_, *P["out"]), residual
+    return bench.layer_step(P, hidden, residual.clone(), state, slots, cu)
 
 
 def layer64(hidden, residual, P, state, slots, starts):
@@ -484,23 +476,19 @@ def layer64(hidden, residual, P, state, slots, starts):
         return ((q @ w.double().t()) * s * ws.double()).to(BF)
     h = hidden.double() + residual.double()
     q, s = rows(h / (h.pow(2).mean(-1, keepdim=True) + 1e-6).sqrt() * P["norm"].double())
-    row = product(q, s, *P["in"])
+    row = product(q, s, *P["w_in"])
     q, k, v, gate, ab = row.split([H * d] * 4 + [2 * H], dim=1)
     q, k, v, gate = (t.unflatten(1, (H, d)) for t in (q, k, v, gate))
-    alpha = torch.exp(-torch.nn.functional.softplus(ab[:, :H].float()))
+    alpha = torch.exp(-torch.nn.functional.softplus(ab[:, :H].float() - 4))
     beta = torch.sigmoid(ab[:, H:].float())
     o, pool, _ = rule64(q, k, v, alpha, beta, state, slots, starts, torch.zeros(q.shape, device="cuda"), 1e-6)
     o = o.to(BF).double()
     y = o / (o.pow(2).mean(-1, keepdim=True) + 1e-6).sqrt() * P["head"].double() * gate.double() * torch.sigmoid(gate.double())
-    return product(*rows(y.flatten(1)), *P["out"]), h.to(residual.dtype), pool
+    return product(*rows(y.flatten(1)), *P["w_out"]), h.to(residual.dtype), pool
 
 
-def make_layer(seed=30, H=4, d=128, D=512):
-    g = rng(seed)
-    P = dict(H=H, d=d, norm=1 + 0.1 * randn(g, D), head=1 + 0.1 * randn(g, d))
-    P["in"] = gdn.quantize_int8((randn(g, 4 * H * d + 2 * H, D) / D ** 0.5).to(BF))
-    P["out"] = gdn.quantize_int8((randn(g, D, H * d) / (H * d) ** 0.5).to(BF))
-    return P, g
+def make_layer(seed=30):
+    return bench.layer_weights(4, 128, 512, torch.device("cuda"), seed), rng(seed)
 
 
 def test_layer_of_all_operators():
@@ -640,3 +628,12 @@ def test_nothing_is_recorded_for_gradients_and_leaves_are_refused():
         w = torch.nn.Parameter(torch.ones(64, device="cuda"))
         gdn.add_rms_norm_int8(x, w, x)
     assert not scale.requires_grad
+
+
+def test_bench_line_of_the_layer(capsys):
+    import json
+    import types
+    from test_bench_host import CONTRACT
+    bench.run_decode_layer(types.SimpleNamespace(steps=3, warmup=3, e2e_steps=1, batch=4), 0, 1, 0)
+    line = json.loads(capsys.readouterr().out.strip().splitlines()[-1])
+    assert all(k in line for k in CONTRACT) and line["value"] > 0 and line["e2e"]["value"] > 0
