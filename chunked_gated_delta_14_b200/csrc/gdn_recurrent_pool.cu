@@ -103,34 +103,26 @@ __device__ __forceinline__ bool sequence(const PoolParams &p, int s, int *slot, 
 // they (and the squares of k and q, since both sums are linear in them) cross the
 // block in one exchange through shared memory.
 template <int R, bool BF16, bool VEC>
-__global__ void __launch_bounds__(256, 2) recurrent_step_kernel(const PoolParams p, int slices) {
+__device__ __forceinline__ void step(const PoolParams &p, int slot, int64_t t, int h, int slice, int slices) {
     __shared__ float4 sums[2][kGroups][32];
     __shared__ float dots[3][kGroups];
     const int pitch = p.dv / 4, quads = pitch / slices;      // float4 a row, and of this block
     const int group = threadIdx.x / quads, quad = threadIdx.x % quads;
-    const int slice = blockIdx.x % slices, sh = blockIdx.x / slices, s = sh / p.H, h = sh % p.H;
-    int slot, t, end;
-    if (!sequence(p, s, &slot, &t, &end)) return;
     const int col = (slice * quads + quad) * 4;
-    const int64_t oi = ((int64_t)t * p.H + h) * p.dv + col;
-    if (slot < 0) {                      // no sequence: a zero row of o
-        if (group == 0)
-            for (int c = 0; c < 4; ++c) store_o(p, oi + c, 0.f);
-        return;
-    }
+    const int64_t oi = (t * p.H + h) * p.dv + col;
     const int row0 = group * R, hk = h / (p.H / p.Hk);
     float4 *hp = reinterpret_cast<float4 *>(p.state + (((int64_t)slot * p.H + h) * p.dk + row0) * p.dv + col);
     float4 x[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) x[r] = __ldcg(hp + r * pitch);
     Raw<R, BF16> k, q;
-    k.template load<VEC>(p.k, (int64_t)t * p.k_row + (int64_t)hk * p.k_head + row0);
-    q.template load<VEC>(p.q, (int64_t)t * p.q_row + (int64_t)hk * p.q_head + row0);
+    k.template load<VEC>(p.k, t * p.k_row + (int64_t)hk * p.k_head + row0);
+    q.template load<VEC>(p.q, t * p.q_row + (int64_t)hk * p.q_head + row0);
     float v[4];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) v[c] = load1(p.v, (int64_t)t * p.v_row + (int64_t)h * p.v_head + col + c, BF16);
-    const float a = p.alpha ? __ldg(p.alpha + (int64_t)t * p.alpha_row + h) : 1.f;
-    const float be = p.beta ? __ldg(p.beta + (int64_t)t * p.beta_row + h) : 1.f;
+    for (int c = 0; c < 4; ++c) v[c] = load1(p.v, t * p.v_row + (int64_t)h * p.v_head + col + c, BF16);
+    const float a = p.alpha ? __ldg(p.alpha + t * p.alpha_row + h) : 1.f;
+    const float be = p.beta ? __ldg(p.beta + t * p.beta_row + h) : 1.f;
 
     float4 hk4 = make_float4(0.f, 0.f, 0.f, 0.f), hq4 = hk4;
     float kk = 0.f, qq = 0.f, kq = 0.f;
@@ -177,6 +169,19 @@ __global__ void __launch_bounds__(256, 2) recurrent_step_kernel(const PoolParams
         store_o(p, oi + 2, fmaf(b, u[2], aq * y.z));
         store_o(p, oi + 3, fmaf(b, u[3], aq * y.w));
     }
+}
+
+template <int R, bool BF16, bool VEC>
+__global__ void __launch_bounds__(256, 2) recurrent_step_kernel(const PoolParams p, int slices) {
+    const int slice = blockIdx.x % slices, sh = blockIdx.x / slices, s = sh / p.H, h = sh % p.H;
+    int slot, t, end;
+    if (!sequence(p, s, &slot, &t, &end)) return;
+    if (slot < 0) {                      // no sequence: a zero row of o
+        const int wide = p.dv / slices;
+        if ((int)threadIdx.x < wide) store_o(p, ((int64_t)t * p.H + h) * p.dv + slice * wide + threadIdx.x, 0.f);
+        return;
+    }
+    step<R, BF16, VEC>(p, slot, t, h, slice, slices);
 }
 
 __device__ __forceinline__ float xor_add(float x, int mask) { return x + __shfl_xor_sync(~0u, x, mask); }
@@ -271,6 +276,13 @@ __global__ void __launch_bounds__(W * 32, R < 16 ? 1 : LONG ? 8 / W : 12 / W) re
     if (slot < 0) {                      // no sequence: zero rows of o
         for (int64_t t = begin; t < end; ++t)
             if (threadIdx.x < kWide) store_o(p, (t * p.H + h) * p.dv + slice * kWide + threadIdx.x, 0.f);
+        return;
+    }
+    // A single token as in the kernel above, which has no tokens to bring (256 such sequences of 16
+    // heads, 37 of them idle: 80 us, the other way 105); the block has the shape of a step's.
+    if (!LONG && end - begin == 1) {
+        if (p.vec) step<R, BF16, true>(p, slot, begin, h, slice, slices);
+        else step<R, BF16, false>(p, slot, begin, h, slice, slices);
         return;
     }
     const int group = lane >> 2, quad = lane & 3, hk = h / (p.H / p.Hk);
@@ -535,7 +547,7 @@ void launch_r(const PoolParams &p, cudaStream_t stream) {
     unsigned blocks = (unsigned)p.seqs * (unsigned)p.H;
     if (p.cu_seqlens) {
         // LONG where sequences have 16 tokens and more on average: 600 tokens of 16 heads 213 us
-        // (288 the other way); decode steps of 256 x 16 heads 106 us (131).
+        // (288 the other way); 200 sequences of 1 to 8 tokens, 16 heads, 115 us (128).
         const bool is_long = p.rows / 16 >= p.seqs;
         if (p.dv % 64 == 0) launch_ragged<R, BF16, 4>(p, is_long, blocks * (p.dv / 64), stream);
         else launch_ragged<R, BF16, 2>(p, is_long, blocks * (p.dv / 32), stream);
