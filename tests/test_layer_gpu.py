@@ -163,6 +163,19 @@ def test_recurrent_ragged_pool(io, packed, unit, o_dtype, dk, dv, Hk, H):
         assert torch.equal(state[i], before[i])
 
 
+def test_recurrent_of_nothing():
+    none = torch.zeros(0, 2, 64, device="cuda")
+    state = randn(rng(45), 3, 2, 64, 64)
+    before = state.clone()
+    cu = lambda *n: torch.tensor(n, dtype=torch.int32, device="cuda")  # noqa: E731
+    assert gdn.recurrent_fwd(none, none, none, None, None, state).shape == (0, 2, 64)
+    gdn.recurrent_fwd(none, none, none, None, None, state, None, cu(0, 0, 0))
+    x = randn(rng(46), 4, 2, 64)
+    o = gdn.recurrent_fwd(x, x, x, None, None, state, None, cu(0))
+    o2 = gdn.recurrent_fwd(x, x, x, None, None, state, cu(2, 1), cu(3, 3, 3))
+    assert not o.any() and not o2.any() and torch.equal(state, before)
+
+
 def test_recurrent_made_output_is_zero_behind_the_last_sequence():
     q, k, v, al, be, state, starts = make_rule(3, [2, 1], 1, 1, 64, 64, tail=4)
     cu = torch.tensor(starts, dtype=torch.int32, device="cuda")
@@ -378,6 +391,20 @@ def test_rows_with_other_strides_and_dimensions():
         assert q2.shape == x.shape
 
 
+def test_rows_past_32_bits():
+    """More than 2^31 numbers; the rows on both sides of that border and the last."""
+    R, D = 66001, 32768
+    x = torch.empty(R, D, device="cuda", dtype=BF)
+    x[0::2] = 1.0
+    x[1::2] = -3.0
+    some = [0, 65535, 65536, 65537, R - 1]
+    for i in some:
+        x[i] = rows_x(50 + i, (1, D), BF)[0]
+    q, scale = gdn.quantize_int8(x)
+    check_rows(q[some], scale[some], x[some].double())
+    assert (q[2] == 127).all() and (q[R - 2] == -127).all()
+
+
 # ------------------------------------------------------------------ int8_matmul
 
 def check_product(out, x, xs, w, ws, bias, rows=None):
@@ -449,6 +476,16 @@ def test_product_dimensions_output_and_rows_left_alone():
     row = gdn.int8_matmul(x[0], xs[0], w, ws)
     assert row.shape == (50,) and torch.equal(row, out[0])
     assert gdn.int8_matmul(x[:0], xs[:0], w, ws).shape == (0, 50)
+
+
+def test_product_past_32_bits():
+    """An output of more than 2^31 numbers."""
+    M, N, K = 270001, 8192, 32
+    x, xs, w, ws, _ = make_product(24, M, N, K)
+    out = gdn.int8_matmul(x, xs, w, ws)
+    gdn.device_check()
+    for a in (0, 262143 - 128, M - 200):
+        check_product(out[a:a + 200], x[a:a + 200], xs[a:a + 200], w, ws, None)
 
 
 def test_product_of_rows_that_are_not_finite():
