@@ -234,9 +234,9 @@ __device__ __forceinline__ void store_few(float *p, const float (&x)[N]) {
 }
 
 // Ragged sequences.  Columns of h never meet: a block takes one sequence, head and
-// W * 16 columns, and each warp 16 of them through all tokens, with h in registers.
-// Lane = row group (8) x column quad (4), R = d_k / 8 rows by 4 columns, as pairs of
-// rows for the two-float fma.
+// W NQ 16 columns, and each warp 16 NQ of them through all tokens, with h in registers.
+// Lane = row group (8) x column quad (4), R = d_k / 8 rows by 4 columns NQ times, as
+// pairs of rows for the two-float fma.
 //
 // The chain p -> u -> h would cost a token two exchanges over d_k, one after the
 // other, so tokens go in fours, by forward substitution: with h = A g (A the product
@@ -255,12 +255,14 @@ __device__ __forceinline__ void store_few(float *p, const float (&x)[N]) {
 // and form the next ones' dot products, beside the present ones.  A group's rows
 // are interleaved, so that the groups' 16-byte reads of k and q meet in no bank.
 // LONG: two fours between barriers, twice the registers, and the longest sequences
-// first.  48 sequences of 0 to 600 tokens (5155 in all), 32 heads of 128 x 128: 650 us;
-// the fma's alone would take 225 (an f32x2 takes two cycles of its pipe).
-template <int R, bool BF16, int W, bool LONG>
+// first.  NQ = 2 reads a token's k and q once for twice the columns, at 8 warps a SM
+// either way.  48 sequences of 0 to 600 tokens (5155 in all), 32 heads of 128 x 128:
+// 545 us (NQ = 1: 648); the fma's alone would take 225 (an f32x2 takes two cycles of
+// its pipe).
+template <int R, bool BF16, int W, bool LONG, int NQ>
 __global__ void __launch_bounds__(W * 32, R < 16 ? 1 : LONG ? 8 / W : 12 / W) recurrent_ragged_kernel(const PoolParams p) {
     constexpr int kBring = LONG ? 2 * kFour : kFour; // tokens between two barriers
-    constexpr int kDk = R * kGroups, kThreads = W * 32, kWide = W * kCols;
+    constexpr int kDk = R * kGroups, kThreads = W * 32, kWide = W * NQ * kCols;
     constexpr int kRun = R < 4 ? R : 4;              // consecutive rows
     constexpr int kMine = kBring / W;                // tokens of those a warp brings
     constexpr int kPer = (kDk + 31) / 32, kPerV = kWide / 32;   // numbers of k, v a lane brings
@@ -287,10 +289,10 @@ __global__ void __launch_bounds__(W * 32, R < 16 ? 1 : LONG ? 8 / W : 12 / W) re
     }
     const int group = lane >> 2, quad = lane & 3, hk = h / (p.H / p.Hk);
     auto row_of = [&](int r) { return (group + kGroups * (r / kRun)) * kRun + r % kRun; };
-    const int col0 = slice * kWide + warp * kCols;
+    const int col0 = slice * kWide + warp * NQ * kCols;
     float4 *hp = reinterpret_cast<float4 *>(p.state + ((int64_t)slot * p.H + h) * p.dk * p.dv + col0) + quad;
     const int pitch = p.dv / 4;          // float4 a row
-    F2 g[R / 2][4];
+    F2 g[NQ][R / 2][4];
 
     // this warp's tokens of a bring, from memory (zeros behind the end): kPer consecutive
     // numbers of q and k a lane, kPerV of v
@@ -382,17 +384,21 @@ __global__ void __launch_bounds__(W * 32, R < 16 ? 1 : LONG ? 8 / W : 12 / W) re
         }
     };
     // this lane's sums over its rows of g with one token's numbers, by column
-    auto partial = [&](const float *x, float (&y)[4]) {
-        F2 xp[R / 2], acc[4];
+    auto partial = [&](const float *x, float (&y)[NQ][4]) {
+        F2 xp[R / 2];
         rows_at(x, xp);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) acc[c] = mul2(g[0][c], xp[0]);
+        for (int z = 0; z < NQ; ++z) {
+            F2 acc[4];
 #pragma unroll
-        for (int r = 1; r < R / 2; ++r)
+            for (int c = 0; c < 4; ++c) acc[c] = mul2(g[z][0][c], xp[0]);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) acc[c] = fma2(g[r][c], xp[r], acc[c]);
+            for (int r = 1; r < R / 2; ++r)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) y[c] = both(acc[c]);
+                for (int c = 0; c < 4; ++c) acc[c] = fma2(g[z][r][c], xp[r], acc[c]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) y[z][c] = both(acc[c]);
+        }
     };
     // halving exchange over bits 4 and 3: the sum of column 2 (bit 4) + (bit 3)
     const bool hi = lane & 16, odd = lane & 8, is_q = lane & 4;
@@ -402,7 +408,7 @@ __global__ void __launch_bounds__(W * 32, R < 16 ? 1 : LONG ? 8 / W : 12 / W) re
         return (odd ? c : a) + __shfl_xor_sync(~0u, odd ? a : c, 8);
     };
 
-    const int mine = warp * kCols + quad * 4 + 2 * hi + odd;      // the lane's column after it
+    const int mine = warp * NQ * kCols + quad * 4 + 2 * hi + odd; // the lane's (first) column after it
     const int64_t o_row = (int64_t)p.H * p.dv;
     int64_t oi = ((int64_t)begin * p.H + h) * p.dv + slice * kWide + mine;
     float A = 1.f;
@@ -414,52 +420,75 @@ __global__ void __launch_bounds__(W * 32, R < 16 ? 1 : LONG ? 8 / W : 12 / W) re
         if (ALL) i0 = 0;
         const int at = f + i0;
         auto has = [&](int i) { return ALL || i < cnt; };
-        float sum[kFour], u[kFour];      // P in the lanes with bit 2 clear, Q in those with it set
+        float sum[NQ][kFour], u[NQ][kFour];      // P in the lanes with bit 2 clear, Q in those with it set
 #pragma unroll
         for (int i = 0; i < kFour; ++i) {
-            float P[4] = {0.f, 0.f, 0.f, 0.f}, Q[4] = {0.f, 0.f, 0.f, 0.f};
-            if (has(i)) { partial(ks[b][at + i], P); partial(qs[b][at + i], Q); }
-            const float x = halve(P), y = halve(Q);
-            sum[i] = (is_q ? y : x) + __shfl_xor_sync(~0u, is_q ? x : y, 4);
+            float P[NQ][4], Q[NQ][4];
+            if (has(i)) {
+                partial(ks[b][at + i], P);
+                partial(qs[b][at + i], Q);
+            } else {
+#pragma unroll
+                for (int z = 0; z < NQ; ++z)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) P[z][c] = Q[z][c] = 0.f;
+            }
+#pragma unroll
+            for (int z = 0; z < NQ; ++z) {
+                const float x = halve(P[z]), y = halve(Q[z]);
+                sum[z][i] = (is_q ? y : x) + __shfl_xor_sync(~0u, is_q ? x : y, 4);
+            }
         }
         // u' where P is, then across to where Q is
 #pragma unroll
-        for (int i = 0; i < kFour; ++i) {
-            float y = sum[i];
+        for (int z = 0; z < NQ; ++z) {
 #pragma unroll
-            for (int j = 0; j < i; ++j)
-                if (has(i)) y = fmaf(kk[d][at + i][i0 + j], u[j], y);
-            u[i] = has(i) ? betas[b][at + i] * (__fdividef(vs[b][at + i][mine], Ai[i]) - y) : 0.f;
-        }
+            for (int i = 0; i < kFour; ++i) {
+                float y = sum[z][i];
 #pragma unroll
-        for (int i = 0; i < kFour; ++i) {
-            const float y = __shfl_xor_sync(~0u, u[i], 4);
-            if (is_q) u[i] = y;
+                for (int j = 0; j < i; ++j)
+                    if (has(i)) y = fmaf(kk[d][at + i][i0 + j], u[z][j], y);
+                u[z][i] = has(i) ? betas[b][at + i] * (__fdividef(vs[b][at + i][mine + z * kCols], Ai[i]) - y) : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < kFour; ++i) {
+                const float y = __shfl_xor_sync(~0u, u[z][i], 4);
+                if (is_q) u[z][i] = y;
+            }
         }
 #pragma unroll
         for (int i = 0; i < kFour; ++i)
             if (has(i)) {
-                float y = sum[i];
 #pragma unroll
-                for (int j = 0; j <= i; ++j) y = fmaf(kq[d][at + i][i0 + j], u[j], y);
-                if (is_q) store_o(p, oi, Ai[i] * y);
+                for (int z = 0; z < NQ; ++z) {
+                    float y = sum[z][i];
+#pragma unroll
+                    for (int j = 0; j <= i; ++j) y = fmaf(kq[d][at + i][i0 + j], u[z][j], y);
+                    if (is_q) store_o(p, oi + z * kCols, Ai[i] * y);
+                }
                 oi += o_row;
             }
 #pragma unroll
         for (int i = 0; i < kFour; ++i) {
-            const float un = __shfl_xor_sync(~0u, u[i], 8);
-            const float u0 = odd ? un : u[i], u1 = odd ? u[i] : un;
-            const float w0 = __shfl_xor_sync(~0u, u0, 16), w1 = __shfl_xor_sync(~0u, u1, 16);
-            const float y[4] = {hi ? w0 : u0, hi ? w1 : u1, hi ? u0 : w0, hi ? u1 : w1};
+            float y[NQ][4];
+#pragma unroll
+            for (int z = 0; z < NQ; ++z) {
+                const float un = __shfl_xor_sync(~0u, u[z][i], 8);
+                const float u0 = odd ? un : u[z][i], u1 = odd ? u[z][i] : un;
+                const float w0 = __shfl_xor_sync(~0u, u0, 16), w1 = __shfl_xor_sync(~0u, u1, 16);
+                y[z][0] = hi ? w0 : u0; y[z][1] = hi ? w1 : u1; y[z][2] = hi ? u0 : w0; y[z][3] = hi ? u1 : w1;
+            }
             if (has(i)) {
                 F2 kp[R / 2];
                 rows_at(ks[b][at + i], kp);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const F2 uu = pack(y[c], y[c]);
+                for (int z = 0; z < NQ; ++z)
 #pragma unroll
-                    for (int r = 0; r < R / 2; ++r) g[r][c] = fma2(kp[r], uu, g[r][c]);
-                }
+                    for (int c = 0; c < 4; ++c) {
+                        const F2 uu = pack(y[z][c], y[z][c]);
+#pragma unroll
+                        for (int r = 0; r < R / 2; ++r) g[z][r][c] = fma2(kp[r], uu, g[z][r][c]);
+                    }
             }
         }
     };
@@ -467,24 +496,31 @@ __global__ void __launch_bounds__(W * 32, R < 16 ? 1 : LONG ? 8 / W : 12 / W) re
     auto into_g = [&](float x) {
         const F2 f = pack(x, x);
 #pragma unroll
-        for (int r = 0; r < R / 2; ++r)
+        for (int z = 0; z < NQ; ++z)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) g[r][c] = mul2(g[r][c], f);
+            for (int r = 0; r < R / 2; ++r)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) g[z][r][c] = mul2(g[z][r][c], f);
     };
 
     const int brings = (end - begin + kBring - 1) / kBring;
     fetch(0);                            // before the state: it is needed first
-    float4 rows[R];
+    float4 rows[NQ][R];
 #pragma unroll
-    for (int r = 0; r < R; ++r) rows[r] = __ldcg(hp + row_of(r) * pitch);
+    for (int z = 0; z < NQ; ++z)
+#pragma unroll
+        for (int r = 0; r < R; ++r) rows[z][r] = __ldcg(hp + row_of(r) * pitch + z * (kCols / 4));
     keep(0);
     if (brings > 1) { fetch(1); keep(1); }
     if (brings > 2) fetch(2);
 #pragma unroll
-    for (int r = 0; r < R; r += 2) {
-        g[r / 2][0] = pack(rows[r].x, rows[r + 1].x); g[r / 2][1] = pack(rows[r].y, rows[r + 1].y);
-        g[r / 2][2] = pack(rows[r].z, rows[r + 1].z); g[r / 2][3] = pack(rows[r].w, rows[r + 1].w);
-    }
+    for (int z = 0; z < NQ; ++z)
+#pragma unroll
+        for (int r = 0; r < R; r += 2) {
+            const float4 x = rows[z][r], y = rows[z][r + 1];
+            g[z][r / 2][0] = pack(x.x, y.x); g[z][r / 2][1] = pack(x.y, y.y);
+            g[z][r / 2][2] = pack(x.z, y.z); g[z][r / 2][3] = pack(x.w, y.w);
+        }
     __syncthreads();
     dots(0, 0);
     __syncthreads();
@@ -528,19 +564,21 @@ __global__ void __launch_bounds__(W * 32, R < 16 ? 1 : LONG ? 8 / W : 12 / W) re
         b = next;
     }
 #pragma unroll
-    for (int r = 0; r < R; r += 2) {
-        float x[4], y[4];
+    for (int z = 0; z < NQ; ++z)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) unpack(g[r / 2][c], &x[c], &y[c]);
-        __stcg(hp + row_of(r) * pitch, make_float4(A * x[0], A * x[1], A * x[2], A * x[3]));
-        __stcg(hp + row_of(r + 1) * pitch, make_float4(A * y[0], A * y[1], A * y[2], A * y[3]));
-    }
+        for (int r = 0; r < R; r += 2) {
+            float x[4], y[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) unpack(g[z][r / 2][c], &x[c], &y[c]);
+            __stcg(hp + row_of(r) * pitch + z * (kCols / 4), make_float4(A * x[0], A * x[1], A * x[2], A * x[3]));
+            __stcg(hp + row_of(r + 1) * pitch + z * (kCols / 4), make_float4(A * y[0], A * y[1], A * y[2], A * y[3]));
+        }
 }
 
 template <int R, bool BF16, int W>
 void launch_ragged(const PoolParams &p, bool is_long, unsigned blocks, cudaStream_t stream) {
-    if (is_long) recurrent_ragged_kernel<R, BF16, W, true><<<blocks, W * 32, 0, stream>>>(p);
-    else recurrent_ragged_kernel<R, BF16, W, false><<<blocks, W * 32, 0, stream>>>(p);
+    if (is_long) recurrent_ragged_kernel<R, BF16, W, true, 1><<<blocks, W * 32, 0, stream>>>(p);
+    else recurrent_ragged_kernel<R, BF16, W, false, 1><<<blocks, W * 32, 0, stream>>>(p);
 }
 template <int R, bool BF16>
 void launch_r(const PoolParams &p, cudaStream_t stream) {
@@ -549,7 +587,10 @@ void launch_r(const PoolParams &p, cudaStream_t stream) {
         // LONG where sequences have 16 tokens and more on average: 600 tokens of 16 heads 213 us
         // (288 the other way); 200 sequences of 1 to 8 tokens, 16 heads, 115 us (128).
         const bool is_long = p.rows / 16 >= p.seqs;
-        if (p.dv % 64 == 0) launch_ragged<R, BF16, 4>(p, is_long, blocks * (p.dv / 64), stream);
+        // Two column quads a lane where whole heads still fill the SMs twice (48 sequences x 32
+        // heads 545 us, with one 648); fewer are quicker on more blocks.
+        if (is_long && p.dv == 128 && blocks >= 296) recurrent_ragged_kernel<R, BF16, 4, true, 2><<<blocks, 128, 0, stream>>>(p);
+        else if (p.dv % 64 == 0) launch_ragged<R, BF16, 4>(p, is_long, blocks * (p.dv / 64), stream);
         else launch_ragged<R, BF16, 2>(p, is_long, blocks * (p.dv / 32), stream);
     } else {
         // 64 columns a block (256 x 16 heads of 128 x 128: 86 us; 128 columns 90, 32 columns 90);

@@ -193,16 +193,18 @@ def test_recurrent_without_gates_and_with_unaligned_rows():
     check_rule(o, state, want, range(2), starts, q, 128, 5)
 
 
-@pytest.mark.parametrize("dk,dv", [(128, 128), (32, 96)])
-def test_recurrent_long_sequences_of_many_lengths(dk, dv):
-    """Lengths whose mean is over 16, where the blocks take the longest sequences first."""
+@pytest.mark.parametrize("dk,dv,Hk,H,io", [(128, 128, 1, 1, F), (32, 96, 1, 1, F), (128, 128, 1, 3, BF), (128, 128, 3, 3, F),
+                                           (16, 128, 1, 4, BF), (64, 128, 1, 3, F)])
+def test_recurrent_long_sequences_of_many_lengths(dk, dv, Hk, H, io):
+    """Lengths whose mean is over 16, where the blocks take the longest sequences first, and from
+    296 sequences and heads on two column quads a lane."""
     g = torch.Generator().manual_seed(8)
     lens = [1, 0, 200, 63, 64, 65, 2] + torch.randint(0, 60, (140,), generator=g).tolist()
     slots = torch.randperm(160, generator=g)[:len(lens)].tolist()
     slots[3] = slots[40] = -1
-    q, k, v, al, be, state, starts = make_rule(8, lens, 1, 1, dk, dv, F, pool=160, tail=4)
+    q, k, v, al, be, state, starts = make_rule(8, lens, Hk, H, dk, dv, io, pool=160, tail=4)
     assert starts[-1] >= 16 * len(lens)
-    out = torch.full(v.shape, 5.0, device="cuda")
+    out = torch.full(v.shape, 5.0, device="cuda", dtype=io)
     want = rule64(q, k, v, al, be, state, slots, starts, out)
     gdn.recurrent_fwd(q, k, v, al, be, state, torch.tensor(slots, dtype=torch.int32, device="cuda"),
                       torch.tensor(starts, dtype=torch.int32, device="cuda"), out=out)
@@ -211,11 +213,11 @@ def test_recurrent_long_sequences_of_many_lengths(dk, dv):
     assert (out[starts[-1]:] == 5).all() and (out[starts[3]:starts[4]] == 0).all()
 
 
-@pytest.mark.parametrize("dk,dv", [(128, 128), (16, 32)])
-def test_recurrent_decays_of_any_size(dk, dv):
+@pytest.mark.parametrize("dk,dv,H", [(128, 128, 2), (16, 32, 2), (128, 128, 60)])
+def test_recurrent_decays_of_any_size(dk, dv, H):
     """Decays of 0 and near it, and long runs of small ones: no product of theirs is divided by."""
-    lens = [37, 13, 1, 1, 4]
-    q, k, v, al, be, state, starts = make_rule(9, lens, 1, 2, dk, dv, F)
+    lens = [67, 13, 1, 1, 4]
+    q, k, v, al, be, state, starts = make_rule(9, lens, 1, H, dk, dv, F)
     g = rng(10)
     pick = torch.tensor([0.0, 1e-38, 1e-30, 1e-12, 1e-6, 0.01, 0.5, 1.0], device="cuda")
     al = pick[torch.randint(0, 8, al.shape, device="cuda", generator=g)]
