@@ -184,7 +184,7 @@ int8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     __shared__ __align__(8) uint64_t full[C::kStages], empty[C::kStages], acc_full[2], acc_empty[2], drain;
-    __shared__ __align__(16) float x_scales[2][BN];
+    __shared__ __align__(16) float x_scales[4][BN];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     volatile int *abort = &abort_flag;
@@ -276,10 +276,12 @@ int8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             const bool has = row < g.channels && n < p.N;
             const float ws = has ? __ldg(p.w_scale + n) : 0.f;
             const float b = has && p.bias ? __ldg(p.bias + n) : 0.f;
-            // the tokens' scales, while the sums are formed (the buffer's last reader was two tiles ago)
-            for (int j = threadIdx.x - 64; j < BN; j += 128) x_scales[acc][j] = m0 + j < p.M ? __ldg(p.x_scale + m0 + j) : 0.f;
-            named_bar(1, 128);
-            if (!mbar_wait_cluster(&acc_full[acc], (i / 2) & 1, abort, 5, kLimit)) break;
+            // the tokens' scales, a copy for each warp, while the sums are formed: the four warps have
+            // no barrier among them that one which gives up could leave the others in
+            __syncwarp();
+            for (int j = lane; j < BN; j += 32) x_scales[quarter][j] = m0 + j < p.M ? __ldg(p.x_scale + m0 + j) : 0.f;
+            __syncwarp();
+            if (!__all_sync(~0u, mbar_wait_cluster(&acc_full[acc], (i / 2) & 1, abort, 5, kLimit))) break;
             tc_fence_after();
             const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + acc * BN;
             constexpr int kCols = BN < 32 ? 16 : 32;
@@ -292,7 +294,7 @@ int8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                 tmem_wait_ld();
                 const int left = min(kCols, p.M - m0 - c);
                 const int64_t o = (int64_t)(m0 + c) * p.out_row + n;
-                const float *xs = &x_scales[acc][c];
+                const float *xs = &x_scales[quarter][c];
                 if (!has) continue;
                 if (left == kCols) {
                     if (p.out_bf16) store_column<kCols>(reinterpret_cast<__nv_bfloat16 *>(p.out) + o, p.out_row, r, xs, ws, b);

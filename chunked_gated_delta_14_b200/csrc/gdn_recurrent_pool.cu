@@ -200,6 +200,7 @@ __device__ __forceinline__ int longest_first(const PoolParams &p, int rank) {
         return n > 0 ? __clz(n) : 32;
     };
     if (threadIdx.x < 33) count[threadIdx.x] = 0;
+    if (threadIdx.x == 0) found = rank;      // (a sequence whatever happens to cu_seqlens meanwhile)
     __syncthreads();
     for (int s = threadIdx.x; s < p.seqs; s += THREADS) atomicAdd(&count[bucket(s)], 1);
     __syncthreads();
