@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(W * 32, R < 16 ? 1 : LONG ? 8 / W : 12 / W) re
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slices = p.dv / kWide;
     const int slice = blockIdx.x % slices, h = blockIdx.x / slices % p.H;
     int s = blockIdx.x / slices / p.H;
-    if (LONG) s = longest_first<kThreads>(p, s);
+    if (LONG && p.seqs <= 512) s = longest_first<kThreads>(p, s);     // (of more, the last is a small part)
     int slot, begin, end;
     if (!sequence(p, s, &slot, &begin, &end)) return;
     if (slot < 0) {                      // no sequence: zero rows of o

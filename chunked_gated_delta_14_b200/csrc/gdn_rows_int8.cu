@@ -35,13 +35,13 @@ struct Words {                           // 8 numbers as 32-bit words
     static constexpr int kCount = 2 * sizeof(T);
 };
 
-// 8 numbers from words.
+// 8 numbers from words, as pairs.
 template <typename T>
-__device__ __forceinline__ void widen(const uint32_t (&w)[Words<T>::kCount], float (&x)[8]) {
+__device__ __forceinline__ void widen(const uint32_t (&w)[Words<T>::kCount], F2 (&x)[4]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if constexpr (sizeof(T) == 4) x[i] = __uint_as_float(w[i]);
-        else x[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 4) x[i] = pack(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+        else x[i] = pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
     }
 }
 __device__ __forceinline__ void put(float *p, float x) { *p = x; }
@@ -102,8 +102,11 @@ __device__ __forceinline__ void zero(uint32_t (&w)[N]) {
 }
 
 template <bool VEC, typename T>
-__device__ __forceinline__ void store8(T *row, int i, int width, const float (&x)[8]) {
+__device__ __forceinline__ void store8(T *row, int i, int width, const F2 (&pairs)[4]) {
     uint32_t w[Words<T>::kCount];
+    float x[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) unpack(pairs[k], &x[2 * k], &x[2 * k + 1]);
 #pragma unroll
     for (int k = 0; k < Words<T>::kCount; ++k) {
         if constexpr (sizeof(T) == 4) w[k] = __float_as_uint(x[k]);
@@ -142,11 +145,15 @@ __device__ __forceinline__ void weight8(const T *weight, int i, int width, bool 
     }
 }
 
-// max(top, |x|), NaN if either is.
-__device__ __forceinline__ float top_of(float top, float x) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(top), "f"(fabsf(x)));
-    return r;
+// max(top, |x|) of 8 numbers, NaN if any is.
+__device__ __forceinline__ float top_of(float top, const F2 (&x)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        unpack(x[i], &lo, &hi);
+        asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(lo), "f"(hi));
+    }
+    return top;
 }
 
 // 1 / x to an ulp or two, for normal x whose reciprocal is normal.
@@ -174,13 +181,13 @@ __device__ __forceinline__ float scale_of(float top, float *factor) {
 // rounded first: of a row's bf16 numbers many are half the largest, 63.5 steps, and the
 // rounding puts the product back on that tie where f is a little off.
 template <bool VEC>
-__device__ __forceinline__ void store_steps8(int8_t *row, int i, int width, const float (&y)[8], float f, bool on8) {
+__device__ __forceinline__ void store_steps8(int8_t *row, int i, int width, const F2 (&y)[4], float f, bool on8) {
     uint32_t b[8];
     const F2 ff = pack(f, f), magic = pack(12582912.f, 12582912.f);
 #pragma unroll
     for (int e = 0; e < 8; e += 2) {
         float lo, hi;
-        unpack(add2(mul2(pack(y[e], y[e + 1]), ff), magic), &lo, &hi);
+        unpack(add2(mul2(y[e / 2], ff), magic), &lo, &hi);
         b[e] = __float_as_uint(lo);
         b[e + 1] = __float_as_uint(hi);
     }
@@ -197,21 +204,25 @@ __device__ __forceinline__ void store_steps8(int8_t *row, int i, int width, cons
 }
 // A row without steps: zeros, also where it holds what is not finite.
 template <int V>
-__device__ __forceinline__ void clear(float (&y)[V][8]) {
+__device__ __forceinline__ void clear(F2 (&y)[V][4]) {
 #pragma unroll
     for (int j = 0; j < V; ++j)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[j][e] = 0.f;
+        for (int e = 0; e < 4; ++e) y[j][e] = pack(0.f, 0.f);
 }
-__device__ __forceinline__ float squares(const float (&x)[8]) {
-    F2 sum = mul2(pack(x[0], x[1]), pack(x[0], x[1]));
+__device__ __forceinline__ float squares(const F2 (&x)[4]) {
+    F2 sum = mul2(x[0], x[0]);
 #pragma unroll
-    for (int e = 2; e < 8; e += 2) sum = fma2(pack(x[e], x[e + 1]), pack(x[e], x[e + 1]), sum);
+    for (int e = 1; e < 4; ++e) sum = fma2(x[e], x[e], sum);
     return both(sum);
 }
-__device__ __forceinline__ void times(float (&x)[8], const float (&y)[8]) {
+__device__ __forceinline__ void times(F2 (&x)[4], const F2 (&y)[4]) {
 #pragma unroll
-    for (int e = 0; e < 8; e += 2) unpack(mul2(pack(x[e], x[e + 1]), pack(y[e], y[e + 1])), &x[e], &x[e + 1]);
+    for (int e = 0; e < 4; ++e) x[e] = mul2(x[e], y[e]);
+}
+__device__ __forceinline__ void times(F2 (&x)[4], float y) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = mul2(x[e], pack(y, y));
 }
 
 // Sum and largest over the row's threads (blockDim.x of them, whole warps).  As whole
@@ -265,28 +276,28 @@ __global__ void __launch_bounds__(MOST) rows_kernel(const RowsParams p) {
             if (NORM && p.weight) weight8<VEC>(reinterpret_cast<const WT *>(p.weight), at(j), width, p.weight_vec, ww[j]);
         }
     }
-    float h[V][8], sum = 0.f, top = 0.f;
+    F2 h[V][4];
+    float sum = 0.f, top = 0.f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         widen<XT>(xw[j], h[j]);
         if constexpr (RES) {
-            float b[8];
+            F2 b[4];
             widen<R1>(rw[j], b);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) h[j][e] += b[e];
+            for (int e = 0; e < 4; ++e) h[j][e] = add2(h[j][e], b[e]);
             if (at(j) < width)
                 store8<VEC>(reinterpret_cast<R1 *>(p.residual_out) + r * p.residual_out_row, at(j), width, h[j]);
         }
         if constexpr (NORM) {
             sum += squares(h[j]);
             if (p.weight) {
-                float w[8];
+                F2 w[4];
                 widen<WT>(ww[j], w);
                 times(h[j], w);
             }
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) top = top_of(top, h[j][e]);
+        top = top_of(top, h[j]);
     }
     const Totals t = row_totals<NORM>(sum, top);
     if (!width) return;
@@ -300,9 +311,7 @@ __global__ void __launch_bounds__(MOST) rows_kernel(const RowsParams p) {
     else if (NORM && f * norm < __uint_as_float(kInfBits)) f *= norm;
     else if (NORM)
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) h[j][e] *= norm;
+        for (int j = 0; j < V; ++j) times(h[j], norm);
     int8_t *q = p.q + r * p.q_row;
 #pragma unroll
     for (int j = 0; j < V; ++j)
@@ -333,7 +342,7 @@ __global__ void __launch_bounds__(MOST) gated_kernel(const RowsParams p, int lan
             load8<VEC>(g, at(j), p.width, gw[j]);
         }
     }
-    float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+    F2 w[4] = {pack(1.f, 1.f), pack(1.f, 1.f), pack(1.f, 1.f), pack(1.f, 1.f)};
     if (p.weight && part < p.head) {
         if (p.weight_bf16) {
             uint32_t ww[4];
@@ -345,7 +354,8 @@ __global__ void __launch_bounds__(MOST) gated_kernel(const RowsParams p, int lan
             widen<float>(ww, w);
         }
     }
-    float y[V][8], norm[V], top = 0.f;
+    F2 y[V][4];
+    float norm[V], top = 0.f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         widen<XT>(xw[j], y[j]);
@@ -359,20 +369,21 @@ __global__ void __launch_bounds__(MOST) gated_kernel(const RowsParams p, int lan
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         const float n = rsqrtf(fmaf(norm[j], p.inverse, p.eps));
-        float gate[8];
+        F2 gate[4];
         widen<XT>(gw[j], gate);
         // g / (1 + e^-g): an approximate exponential and quotient, off by some 2^-22 of the
         // result for |g| < 20 (an error of the exponent counts |g| times), against steps of 2^-7
-        float silu[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) silu[e] = rcp(1.f + sm100::ex2_approx(gate[e] * -1.44269504f));
-        times(silu, gate);
-        const float nn[8] = {n, n, n, n, n, n, n, n};
-        times(y[j], nn);
+        for (int e = 0; e < 4; ++e) {
+            float lo, hi;
+            unpack(mul2(gate[e], pack(-1.44269504f, -1.44269504f)), &lo, &hi);
+            unpack(add2(pack(sm100::ex2_approx(lo), sm100::ex2_approx(hi)), pack(1.f, 1.f)), &lo, &hi);
+            gate[e] = mul2(gate[e], pack(rcp(lo), rcp(hi)));
+        }
+        times(y[j], n);
         times(y[j], w);
-        times(y[j], silu);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) top = top_of(top, y[j][e]);
+        times(y[j], gate);
+        top = top_of(top, y[j]);
     }
     const Totals t = row_totals<false>(0.f, top);
     if (!on) return;

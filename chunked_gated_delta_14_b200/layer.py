@@ -178,7 +178,7 @@ def recurrent_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, alpha: Opti
 
     Returns o [N, H, dv] in ``o_dtype`` (default: q's): 0 for entries of slot -1; rows of
     no sequence are left as they were in ``out``, and are 0 where ``out`` is made here.
-    ``qk_norm_eps``: q and k are divided by sqrt(sum of squares + qk_norm_eps) first.
+    ``qk_norm_eps`` (> 0): q and k are divided by sqrt(sum of squares + qk_norm_eps) first.
 
     slots and cu_seqlens are read on the device: an entry out of bounds touches nothing
     and is reported by ``device_check``.  A slot may be named once in a call.  Prompts

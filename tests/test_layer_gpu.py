@@ -213,6 +213,18 @@ def test_recurrent_long_sequences_of_many_lengths(dk, dv, Hk, H, io):
     assert (out[starts[-1]:] == 5).all() and (out[starts[3]:starts[4]] == 0).all()
 
 
+def test_recurrent_many_long_sequences():
+    """More than 512 sequences of 16 tokens and more on average."""
+    lens = [20, 0, 33] + [17] * 540
+    slots = list(range(len(lens)))[::-1]
+    q, k, v, al, be, state, starts = make_rule(47, lens, 1, 1, 16, 32, F)
+    want = rule64(q, k, v, al, be, state, slots, starts, torch.zeros_like(v))
+    o = gdn.recurrent_fwd(q, k, v, al, be, state, torch.tensor(slots, dtype=torch.int32, device="cuda"),
+                          torch.tensor(starts, dtype=torch.int32, device="cuda"))
+    gdn.device_check()
+    check_rule(o, state, want, slots, starts, q, 16, max(lens))
+
+
 @pytest.mark.parametrize("dk,dv,H", [(128, 128, 2), (16, 32, 2), (128, 128, 60)])
 def test_recurrent_decays_of_any_size(dk, dv, H):
     """Decays of 0 and near it, and long runs of small ones: no product of theirs is divided by."""
