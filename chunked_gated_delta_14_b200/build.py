@@ -1,4 +1,5 @@
-"""Build libgdn.so in place with nvcc for sm_100a (B200).
+"""Build libgdn.so in place with nvcc for sm_100a (B200), and _layer.so, the quick
+binding of its decode-layer operators, with the host compiler.
 
 Usage: python -m chunked_gated_delta_14_b200.build [--force] [--verbose]
 """
@@ -15,6 +16,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libgdn.so")
+BINDING = os.path.join(HERE, "_layer.so")
+BINDING_SOURCE = os.path.join(CSRC, "layer_binding.cpp")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
@@ -31,7 +34,27 @@ def _stale() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def build_binding(force: bool = False) -> str:
+    """_layer.so: a Python extension over torch's C++ tensors (no kernels, not linked to libgdn.so)."""
+    deps = [BINDING_SOURCE, os.path.join(INCLUDE, "gdn.h")]
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) > max(map(os.path.getmtime, deps)):
+        return BINDING
+    import sysconfig
+    import torch
+    from torch.utils import cpp_extension
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    tmp = BINDING + f".tmp{os.getpid()}"
+    flags = [f"-I{p}" for p in [INCLUDE, *cpp_extension.include_paths(), os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]]
+    subprocess.check_call([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+                           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *flags, BINDING_SOURCE,
+                           "-o", tmp, *[f"-L{p}" for p in cpp_extension.library_paths()], "-lc10", "-lc10_cuda", "-ltorch_cpu",
+                           "-ltorch", "-ltorch_python"])
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_binding(force)
     if not force and not _stale():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"

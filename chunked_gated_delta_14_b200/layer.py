@@ -50,7 +50,7 @@ class Int8MatmulArgs(ctypes.Structure):
 
 def _packer(mirror):
     """``pack(*fields)`` -> the struct's bytes: several times quicker than filling a ctypes
-    struct field by field, which is most of a small call's time."""
+    struct field by field."""
     codes = {_I: "i", _F: "f", _P: "P", _Q: "q", _U: "Q"}
     s = struct.Struct("@" + "".join(codes[t] for _, t in mirror._fields_))
     assert s.size == ctypes.sizeof(mirror), mirror
@@ -64,6 +64,34 @@ _functions = {}
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _empty = torch.empty_strided          # a third quicker than torch.empty
+
+
+class _NoQuick:
+    """In place of the quick binding where it was not built: every call goes the long way."""
+    recurrent_fwd = add_rms_norm_int8 = gated_rms_norm_int8 = quantize_int8 = int8_matmul = staticmethod(lambda *a: None)
+
+
+_quick = None
+
+
+def _bind_quick():
+    """_layer.so (csrc/layer_binding.cpp): the operators' calls of the usual form at a third of
+    the host's time.  What it does not take comes back as None and goes the long way below."""
+    global _quick
+    L = lib()
+    try:
+        from . import _layer
+    except ImportError:
+        _quick = _NoQuick
+    else:
+        _layer.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            L.gdn_recurrent_fwd, L.gdn_rows_int8, L.gdn_int8_matmul, L.gdn_int8_matmul_workspace_bytes)), L.gdn_abi_version())
+        _quick = _layer
+    return _quick
+
+
+def _failed(status):
+    raise GDNError(status, last_error())
 
 
 def _check(t, name, shape, dtypes, device):
@@ -187,8 +215,10 @@ def recurrent_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, alpha: Opti
     if stream is not None:
         return _other_stream(stream, q, (q, k, v, alpha, beta, state, slots, cu_seqlens, out), lambda: recurrent_fwd(
             q, k, v, alpha, beta, state, slots, cu_seqlens, qk_norm_eps=qk_norm_eps, o_dtype=o_dtype, out=out))
-    # What a correct call looks like, tested in place (the tests are most of what a small call
-    # costs); _recurrent_refuse says what is wrong with another.
+    r = (_quick or _bind_quick()).recurrent_fwd(q, k, v, alpha, beta, state, slots, cu_seqlens, qk_norm_eps, o_dtype, out)
+    if r is not None:
+        return r if type(r) is not int else _failed(r)
+    # What a correct call looks like, tested in place; _recurrent_refuse says what is wrong with another.
     try:
         N, Hk, dk = shape = q.shape
         _, H, dv = v.shape
@@ -309,6 +339,9 @@ def add_rms_norm_int8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, re
     if stream is not None:
         return _other_stream(stream, x, (x, weight, residual, residual_out), lambda: add_rms_norm_int8(
             x, weight, residual, eps=eps, residual_out=residual_out))
+    r = (_quick or _bind_quick()).add_rms_norm_int8(x, weight, residual, eps, residual_out)
+    if r is not None:
+        return r if type(r) is not int else _failed(r)
     i, grad, xd = _row_input(x, 1)
     shape, dev = x.shape, x.device
     flat = len(shape) == 2
@@ -394,6 +427,9 @@ def gated_rms_norm_int8(x: torch.Tensor, gate: torch.Tensor, weight: Optional[to
     int8, its rows on 16-byte boundaries; scale: [...] fp32, one for all heads of a row."""
     if stream is not None:
         return _other_stream(stream, x, (x, gate, weight), lambda: gated_rms_norm_int8(x, gate, weight, eps=eps))
+    r = (_quick or _bind_quick()).gated_rms_norm_int8(x, gate, weight, eps)
+    if r is not None:
+        return r if type(r) is not int else _failed(r)
     i, grad, xd = _row_input(x, 2)
     dev = x.device
     shape = x.shape
@@ -423,6 +459,9 @@ def quantize_int8(x: torch.Tensor, *, stream: Optional[torch.cuda.Stream] = None
     whatever D is; scale: [...] fp32, the row's largest absolute value / 127."""
     if stream is not None:
         return _other_stream(stream, x, (x,), lambda: quantize_int8(x))
+    r = (_quick or _bind_quick()).quantize_int8(x)
+    if r is not None:
+        return r if type(r) is not int else _failed(r)
     i, _, xd = _row_input(x, 1)
     D = x.shape[-1]
     rows, xr = _rows(x, "x")
@@ -444,6 +483,9 @@ def int8_matmul(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale
     if stream is not None:
         return _other_stream(stream, x, (x, x_scale, w, w_scale, bias, out), lambda: int8_matmul(
             x, x_scale, w, w_scale, bias, out_dtype=out_dtype, out=out))
+    r = (_quick or _bind_quick()).int8_matmul(x, x_scale, w, w_scale, bias, out_dtype, out)
+    if r is not None:
+        return r if type(r) is not int else _failed(r)
     grad = torch.is_grad_enabled()
     try:
         shape, i = x.shape, x.get_device()

@@ -188,3 +188,22 @@ BF = torch.bfloat16
 def test_python_refusals(call, error):
     with pytest.raises(error):
         call()
+
+
+def test_quick_binding_builds_and_leaves_other_calls_alone():
+    """_layer.so is built beside the library, binds to its ABI only, and gives None for what is
+    not a plain device tensor."""
+    from chunked_gated_delta_14_b200 import build as gbuild
+    gbuild.build_binding()
+    from chunked_gated_delta_14_b200 import _layer
+    assert L._bind_quick() is _layer
+    with pytest.raises(RuntimeError):
+        _layer.bind(0, 0, 0, 0, 1)
+    x = torch.zeros(4, 64)
+    for a in (x, dev(4, 64), [1.0], None):
+        assert _layer.quantize_int8(a) is None
+        assert _layer.add_rms_norm_int8(a, None, None, 1e-6, None) is None
+        assert _layer.gated_rms_norm_int8(a, a, None, 1e-6) is None
+        assert _layer.int8_matmul(a, a, a, a, None, torch.float32, None) is None
+        assert _layer.recurrent_fwd(a, a, a, None, None, a, None, None, None, None, None) is None
+    assert _layer.quantize_int8() is None and _layer.int8_matmul(x) is None

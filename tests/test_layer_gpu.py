@@ -670,6 +670,49 @@ def test_recurrent_gives_the_same_bits_alone_and_in_a_batch():
         assert torch.equal(o1, o[a:e]) and torch.equal(s1[0], s0[i])
 
 
+@pytest.mark.parametrize("quick", [True, False])
+def test_both_ways_to_the_library(quick, monkeypatch):
+    """Calls of every operator through the quick binding and without it."""
+    import chunked_gated_delta_14_b200.layer as L
+    from chunked_gated_delta_14_b200 import _layer
+    gdn.quantize_int8(torch.ones(1, 8, device="cuda"))
+    assert L._quick is _layer
+    calls = []
+    if quick:      # a call of the usual form does not reach the long way
+        monkeypatch.setattr(L, "_launch", lambda *a: calls.append(a))
+    else:
+        monkeypatch.setattr(L, "_quick", L._NoQuick)
+    a, r = rows_x(60, (5, 256), BF), rows_x(61, (5, 256), F)
+    w = 1 + 0.1 * randn(rng(62), 256)
+    check_rows(*gdn.quantize_int8(a), a.double())
+    q, s, h = gdn.add_rms_norm_int8(a, w.to(BF), r, residual_out=r)
+    assert h is r
+    y = r.double()
+    check_rows(q, s, y / (y.pow(2).mean(-1, keepdim=True) + 1e-6).sqrt() * w.to(BF).double())
+    x, gate = a.view(5, 4, 64).double(), a.view(5, 4, 64).double()
+    y = x / (x.pow(2).mean(-1, keepdim=True) + 1e-6).sqrt() * w[:64].double() * gate * torch.sigmoid(gate)
+    check_rows(*gdn.gated_rms_norm_int8(a.view(5, 4, 64), a.view(5, 4, 64), w[:64]), y.flatten(1))
+    for pad in (True, False):
+        x, xs, wq, ws, bias = make_product(63, 9, 70, 130, pad=pad, bias=True)
+        out = torch.empty(9, 70, device="cuda")
+        assert gdn.int8_matmul(x, xs, wq, ws, bias, out_dtype=F, out=out) is out
+        check_product(out, x, xs, wq, ws, bias)
+        check_product(gdn.int8_matmul(x, xs, wq, ws, bias), x, xs, wq, ws, bias)
+    lens, slots = [3, 0, 2], [1, 0, -1]
+    q, k, v, al, be, state, starts = make_rule(64, lens, 1, 2, 64, 64, BF, packed=True)
+    want = rule64(q, k, v, al, be, state, slots, starts, torch.zeros_like(v))
+    o = gdn.recurrent_fwd(q, k, v, al, be, state, torch.tensor(slots, dtype=torch.int32, device="cuda"),
+                          torch.tensor(starts, dtype=torch.int32, device="cuda"), o_dtype=F)
+    assert o.dtype == F
+    check_rule(o, state, want, slots, starts, q, 64, 3)
+    with pytest.raises(gdn.GDNError, match="eps"):
+        gdn.add_rms_norm_int8(a, eps=0.0)
+    with pytest.raises(ValueError):
+        gdn.int8_matmul(x, xs, wq[:, 1:], ws)
+    gdn.device_check()
+    assert not calls
+
+
 def test_nothing_is_recorded_for_gradients_and_leaves_are_refused():
     x = randn(rng(44), 4, 64).requires_grad_()
     with pytest.raises(ValueError, match="gradient"):
