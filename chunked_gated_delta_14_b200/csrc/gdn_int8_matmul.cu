@@ -321,17 +321,16 @@ int8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
 }
 
 // Rows of K bytes at any address and stride -> rows on 16 bytes, of one or both
-// operands (first x's, then w's; a warp a row).  Sixteen bytes a thread, from the five
+// operands (first x's, then w's; a block a row).  Sixteen bytes a thread, from the five
 // aligned words that hold them where those lie in the row, else byte by byte.  The
 // bytes behind a row's K become 0 (they are not read: the tensor map ends at K).
 __global__ void __launch_bounds__(256) pad_rows_kernel(const PadRows x, const PadRows w, int K) {
-    const int64_t job = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (job >= (int64_t)x.rows + w.rows) return;
-    const PadRows &p = job < x.rows ? x : w;
-    const int64_t row = job < x.rows ? job : job - x.rows;
+    const unsigned job = blockIdx.x;
+    const PadRows &p = job < (unsigned)x.rows ? x : w;
+    const int64_t row = job < (unsigned)x.rows ? job : job - x.rows;
     const int8_t *from = p.from + row * p.from_row;
     int8_t *to = p.to + row * p.to_row;
-    for (int k = (threadIdx.x & 31) * 16; k < K; k += 512) {
+    for (int k = threadIdx.x * 16; k < K; k += blockDim.x * 16) {
         uint32_t y[4] = {0, 0, 0, 0};
         const uintptr_t at = reinterpret_cast<uintptr_t>(from + k), word = at & ~(uintptr_t)3;
         if (word >= reinterpret_cast<uintptr_t>(from) && word + 20 <= reinterpret_cast<uintptr_t>(from + K)) {
@@ -439,7 +438,9 @@ cudaError_t launch_int8_matmul(const Int8MatmulParams &p, cudaStream_t stream, c
 }
 
 cudaError_t launch_int8_pad_rows(const PadRows &x, const PadRows &w, int K, cudaStream_t stream) {
-    pad_rows_kernel<<<(unsigned)(((int64_t)x.rows + w.rows + 7) / 8), 256, 0, stream>>>(x, w, K);
+    const int threads = (K + 511) / 512 * 32;
+    if ((int64_t)x.rows + w.rows > 0x7fffffff) return cudaErrorInvalidValue;
+    pad_rows_kernel<<<(unsigned)x.rows + (unsigned)w.rows, threads < 256 ? threads : 256, 0, stream>>>(x, w, K);
     return cudaGetLastError();
 }
 

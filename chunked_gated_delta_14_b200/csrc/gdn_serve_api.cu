@@ -159,7 +159,8 @@ gdn_status resolve_matmul(const gdn_int8_matmul_args *a, MatmulPlan *out) {
     if (!a) return api_fail(GDN_ERR_INVALID_ARG, "args is NULL");
     if (a->M < 0 || a->N < 1 || a->K < 1) return api_fail(GDN_ERR_INVALID_ARG, "M must be >= 0, N and K >= 1 (got %d, %d, %d)", a->M, a->N, a->K);
     if (a->K > 131071) return api_fail(GDN_ERR_UNSUPPORTED, "K must be <= 131071 for the sum to fit 32 bits (got %d)", a->K);
-    if ((int64_t)a->M * a->N > ((int64_t)1 << 40)) return api_fail(GDN_ERR_INVALID_ARG, "M * N too large");
+    if ((int64_t)a->M * a->N > ((int64_t)1 << 40) || (int64_t)a->M + a->N > 0x7fffffff)
+        return api_fail(GDN_ERR_INVALID_ARG, "M * N or M + N too large");
     if (!dtype_ok(a->out_dtype)) return api_fail(GDN_ERR_INVALID_ARG, "out_dtype %d unknown", a->out_dtype);
     if (a->x_row < 0 || a->w_row < 0 || a->out_row < 0) return api_fail(GDN_ERR_INVALID_ARG, "strides must be >= 0");
     MatmulPlan m{};
