@@ -194,6 +194,7 @@ int8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     const int first = blockIdx.x / group, stride = gridDim.x / group;
     const uint32_t stage_tx = PAIR ? 2 * C::kStageBytes : (g.channels + C::kTokens) * kBK;
 
+    grid_next();
     if (threadIdx.x == 0) {
         abort_flag = 0;
         for (int i = 0; i < C::kStages; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
@@ -209,6 +210,7 @@ int8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     if (PAIR) cluster_sync_all();        // the other block's barriers are there
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(~0u, tmem_slot, 0);
+    grid_wait();
 
     if (warp == 0 && elect()) {          // the copies: one thread
         int it = 0;
@@ -325,6 +327,8 @@ int8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
 // aligned words that hold them where those lie in the row, else byte by byte.  The
 // bytes behind a row's K become 0 (they are not read: the tensor map ends at K).
 __global__ void __launch_bounds__(256) pad_rows_kernel(const PadRows x, const PadRows w, int K) {
+    grid_next();
+    grid_wait();
     const unsigned job = blockIdx.x;
     const PadRows &p = job < (unsigned)x.rows ? x : w;
     const int64_t row = job < (unsigned)x.rows ? job : job - x.rows;
@@ -386,18 +390,8 @@ cudaError_t launch_bn(const Int8MatmulParams &p, int channels, int dev, int sms,
         if (e != cudaSuccess) return e;
         if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((tiles < most ? tiles : most) * group));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = C::kSmem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)group;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = PAIR ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, int8_matmul_kernel<BN, PAIR>, wmap, xmap, p, g);
+    return launch(true, int8_matmul_kernel<BN, PAIR>, dim3((unsigned)((tiles < most ? tiles : most) * group)), dim3(kThreads), C::kSmem,
+                        stream, (unsigned)group, wmap, xmap, p, g);
 }
 
 }  // namespace
@@ -440,8 +434,7 @@ cudaError_t launch_int8_matmul(const Int8MatmulParams &p, cudaStream_t stream, c
 cudaError_t launch_int8_pad_rows(const PadRows &x, const PadRows &w, int K, cudaStream_t stream) {
     const int threads = (K + 511) / 512 * 32;
     if ((int64_t)x.rows + w.rows > 0x7fffffff) return cudaErrorInvalidValue;
-    pad_rows_kernel<<<(unsigned)x.rows + (unsigned)w.rows, threads < 256 ? threads : 256, 0, stream>>>(x, w, K);
-    return cudaGetLastError();
+    return launch(true, pad_rows_kernel, dim3((unsigned)x.rows + (unsigned)w.rows), dim3(threads < 256 ? threads : 256), 0, stream, 1, x, w, K);
 }
 
 unsigned int int8_matmul_read_and_clear_error(cudaError_t *err) {

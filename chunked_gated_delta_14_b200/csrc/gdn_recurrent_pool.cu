@@ -173,6 +173,7 @@ __device__ __forceinline__ void step(const PoolParams &p, int slot, int64_t t, i
 
 template <int R, bool BF16, bool VEC>
 __global__ void __launch_bounds__(256, 2) recurrent_step_kernel(const PoolParams p, int slices) {
+    if (p.early) { grid_next(); grid_wait(); }
     const int slice = blockIdx.x % slices, sh = blockIdx.x / slices, s = sh / p.H, h = sh % p.H;
     int slot, t, end;
     if (!sequence(p, s, &slot, &t, &end)) return;
@@ -262,6 +263,7 @@ __device__ __forceinline__ void store_few(float *p, const float (&x)[N]) {
 // its pipe).
 template <int R, bool BF16, int W, bool LONG, int NQ>
 __global__ void __launch_bounds__(W * 32, R < 16 ? 1 : LONG ? 8 / W : 12 / W) recurrent_ragged_kernel(const PoolParams p) {
+    if (p.early) { grid_next(); grid_wait(); }
     constexpr int kBring = LONG ? 2 * kFour : kFour; // tokens between two barriers
     constexpr int kDk = R * kGroups, kThreads = W * 32, kWide = W * NQ * kCols;
     constexpr int kRun = R < 4 ? R : 4;              // consecutive rows
@@ -576,49 +578,52 @@ __global__ void __launch_bounds__(W * 32, R < 16 ? 1 : LONG ? 8 / W : 12 / W) re
         }
 }
 
+template <typename... A, typename... B>
+cudaError_t launch_blocks(void (*kernel)(PoolParams, A...), unsigned blocks, int threads, cudaStream_t stream, PoolParams p, B... args) {
+    p.early = is_early(blocks);
+    return launch(p.early, kernel, dim3(blocks), dim3(threads), 0, stream, 1, p, args...);
+}
 template <int R, bool BF16, int W>
-void launch_ragged(const PoolParams &p, bool is_long, unsigned blocks, cudaStream_t stream) {
-    if (is_long) recurrent_ragged_kernel<R, BF16, W, true, 1><<<blocks, W * 32, 0, stream>>>(p);
-    else recurrent_ragged_kernel<R, BF16, W, false, 1><<<blocks, W * 32, 0, stream>>>(p);
+cudaError_t launch_ragged(const PoolParams &p, bool is_long, unsigned blocks, cudaStream_t stream) {
+    return launch_blocks(is_long ? recurrent_ragged_kernel<R, BF16, W, true, 1> : recurrent_ragged_kernel<R, BF16, W, false, 1>, blocks,
+                         W * 32, stream, p);
 }
 template <int R, bool BF16>
-void launch_r(const PoolParams &p, cudaStream_t stream) {
-    unsigned blocks = (unsigned)p.seqs * (unsigned)p.H;
+cudaError_t launch_r(const PoolParams &p, cudaStream_t stream) {
+    const unsigned blocks = (unsigned)p.seqs * (unsigned)p.H;
     if (p.cu_seqlens) {
         // LONG where sequences have 16 tokens and more on average: 600 tokens of 16 heads 213 us
         // (288 the other way); 200 sequences of 1 to 8 tokens, 16 heads, 115 us (128).
         const bool is_long = p.rows / 16 >= p.seqs;
         // Two column quads a lane where whole heads still fill the SMs twice (48 sequences x 32
         // heads 545 us, with one 648); fewer are quicker on more blocks.
-        if (is_long && p.dv == 128 && blocks >= 296) recurrent_ragged_kernel<R, BF16, 4, true, 2><<<blocks, 128, 0, stream>>>(p);
-        else if (p.dv % 64 == 0) launch_ragged<R, BF16, 4>(p, is_long, blocks * (p.dv / 64), stream);
-        else launch_ragged<R, BF16, 2>(p, is_long, blocks * (p.dv / 32), stream);
-    } else {
-        // 64 columns a block (256 x 16 heads of 128 x 128: 86 us; 128 columns 90, 32 columns 90);
-        // where the heads are fewer than two a SM, 32, so that more SMs take part (16 heads: 2.8 us,
-        // with 64 columns 3.2, with 128 4.2).
-        const int slices = blocks < 296 ? p.dv / 32 : p.dv % 64 ? 1 : p.dv / 64, threads = p.dv / 4 / slices * kGroups;
-        if (p.vec) recurrent_step_kernel<R, BF16, true><<<blocks * slices, threads, 0, stream>>>(p, slices);
-        else recurrent_step_kernel<R, BF16, false><<<blocks * slices, threads, 0, stream>>>(p, slices);
+        if (is_long && p.dv == 128 && blocks >= 296)
+            return launch_blocks(recurrent_ragged_kernel<R, BF16, 4, true, 2>, blocks, 128, stream, p);
+        if (p.dv % 64 == 0) return launch_ragged<R, BF16, 4>(p, is_long, blocks * (p.dv / 64), stream);
+        return launch_ragged<R, BF16, 2>(p, is_long, blocks * (p.dv / 32), stream);
     }
+    // 64 columns a block (256 x 16 heads of 128 x 128: 86 us; 128 columns 90, 32 columns 90);
+    // where the heads are fewer than two a SM, 32, so that more SMs take part (16 heads: 2.8 us,
+    // with 64 columns 3.2, with 128 4.2).
+    const int slices = blocks < 296 ? p.dv / 32 : p.dv % 64 ? 1 : p.dv / 64, threads = p.dv / 4 / slices * kGroups;
+    return launch_blocks(p.vec ? recurrent_step_kernel<R, BF16, true> : recurrent_step_kernel<R, BF16, false>, blocks * slices, threads,
+                         stream, p, slices);
 }
 template <int R>
-void launch_io(const PoolParams &p, cudaStream_t stream) {
-    if (p.io_bf16) launch_r<R, true>(p, stream);
-    else launch_r<R, false>(p, stream);
+cudaError_t launch_io(const PoolParams &p, cudaStream_t stream) {
+    return p.io_bf16 ? launch_r<R, true>(p, stream) : launch_r<R, false>(p, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_recurrent_pool(const PoolParams &p, cudaStream_t stream) {
     switch (p.dk / kGroups) {
-        case 2: launch_io<2>(p, stream); break;
-        case 4: launch_io<4>(p, stream); break;
-        case 8: launch_io<8>(p, stream); break;
-        case 16: launch_io<16>(p, stream); break;
-        default: return cudaErrorInvalidValue;
+        case 2: return launch_io<2>(p, stream);
+        case 4: return launch_io<4>(p, stream);
+        case 8: return launch_io<8>(p, stream);
+        case 16: return launch_io<16>(p, stream);
     }
-    return cudaGetLastError();
+    return cudaErrorInvalidValue;
 }
 
 unsigned int pool_read_and_clear_error(cudaError_t *err) {

@@ -257,6 +257,7 @@ __device__ __forceinline__ Totals row_totals(float sum, float top_value) {
 // Thread i takes the eights i, i + blockDim.x, ... of its row.
 template <bool NORM, typename XT, typename RT, typename WT, int V, int MOST, bool VEC>
 __global__ void __launch_bounds__(MOST) rows_kernel(const RowsParams p) {
+    if (p.early) { grid_next(); grid_wait(); }
     constexpr bool RES = !std::is_void<RT>::value;
     using R1 = typename std::conditional<RES, RT, float>::type;
     const int row = blockIdx.x * blockDim.y + threadIdx.y;
@@ -323,6 +324,7 @@ __global__ void __launch_bounds__(MOST) rows_kernel(const RowsParams p) {
 // apart.
 template <typename XT, int V, int MOST, bool VEC>
 __global__ void __launch_bounds__(MOST) gated_kernel(const RowsParams p, int lanes_log2, int heads) {
+    if (p.early) { grid_next(); grid_wait(); }
     const int row = blockIdx.x * blockDim.y + threadIdx.y;
     const bool on = row < p.rows;
     const int64_t r = on ? row : 0;
@@ -401,40 +403,40 @@ struct Launch {
     dim3 grid, block;
     cudaStream_t stream;
     int lanes_log2;
+
+    template <typename... A, typename... B>
+    cudaError_t operator()(void (*kernel)(A...), B... args) const {
+        return launch(is_early(grid.x), kernel, grid, block, 0, stream, 1, args...);
+    }
 };
 template <bool NORM, typename XT, typename RT, typename WT, int V, int MOST>
-void launch_rows(const RowsParams &p, const Launch &l) {
-    if (p.vec) rows_kernel<NORM, XT, RT, WT, V, MOST, true><<<l.grid, l.block, 0, l.stream>>>(p);
-    else rows_kernel<NORM, XT, RT, WT, V, MOST, false><<<l.grid, l.block, 0, l.stream>>>(p);
+cudaError_t launch_rows(const RowsParams &p, const Launch &l) {
+    return p.vec ? l(rows_kernel<NORM, XT, RT, WT, V, MOST, true>, p) : l(rows_kernel<NORM, XT, RT, WT, V, MOST, false>, p);
 }
 template <typename XT, typename WT, int V, int MOST>
-void launch_norm(const RowsParams &p, const Launch &l) {
-    if (!p.residual) launch_rows<true, XT, void, WT, V, MOST>(p, l);
-    else if (p.residual_bf16) launch_rows<true, XT, __nv_bfloat16, WT, V, MOST>(p, l);
-    else launch_rows<true, XT, float, WT, V, MOST>(p, l);
+cudaError_t launch_norm(const RowsParams &p, const Launch &l) {
+    if (!p.residual) return launch_rows<true, XT, void, WT, V, MOST>(p, l);
+    if (p.residual_bf16) return launch_rows<true, XT, __nv_bfloat16, WT, V, MOST>(p, l);
+    return launch_rows<true, XT, float, WT, V, MOST>(p, l);
 }
 template <typename XT, int V, int MOST>
-void launch_x(const RowsParams &p, const Launch &l) {
-    if (p.op == GDN_ROWS_GATED) {
-        if (p.vec) gated_kernel<XT, V, MOST, true><<<l.grid, l.block, 0, l.stream>>>(p, l.lanes_log2, p.width / p.head);
-        else gated_kernel<XT, V, MOST, false><<<l.grid, l.block, 0, l.stream>>>(p, l.lanes_log2, p.width / p.head);
-    } else if (p.op == GDN_ROWS_PLAIN) {
-        launch_rows<false, XT, void, float, V, MOST>(p, l);
-    } else if (p.weight_bf16) {
-        launch_norm<XT, __nv_bfloat16, V, MOST>(p, l);
-    } else {
-        launch_norm<XT, float, V, MOST>(p, l);
-    }
+cudaError_t launch_x(const RowsParams &p, const Launch &l) {
+    if (p.op == GDN_ROWS_GATED)
+        return p.vec ? l(gated_kernel<XT, V, MOST, true>, p, l.lanes_log2, p.width / p.head)
+                     : l(gated_kernel<XT, V, MOST, false>, p, l.lanes_log2, p.width / p.head);
+    if (p.op == GDN_ROWS_PLAIN) return launch_rows<false, XT, void, float, V, MOST>(p, l);
+    if (p.weight_bf16) return launch_norm<XT, __nv_bfloat16, V, MOST>(p, l);
+    return launch_norm<XT, float, V, MOST>(p, l);
 }
 template <int V, int MOST>
-void launch_v(const RowsParams &p, const Launch &l) {
-    if (p.x_bf16) launch_x<__nv_bfloat16, V, MOST>(p, l);
-    else launch_x<float, V, MOST>(p, l);
+cudaError_t launch_v(const RowsParams &p, const Launch &l) {
+    return p.x_bf16 ? launch_x<__nv_bfloat16, V, MOST>(p, l) : launch_x<float, V, MOST>(p, l);
 }
 
 }  // namespace
 
-cudaError_t launch_rows_int8(const RowsParams &p, cudaStream_t stream) {
+cudaError_t launch_rows_int8(const RowsParams &given, cudaStream_t stream) {
+    RowsParams p = given;
     // threads that a row needs at 8 numbers each
     int lanes_log2 = 0, need = (p.width + 7) / 8;
     if (p.op == GDN_ROWS_GATED) {
@@ -449,11 +451,10 @@ cudaError_t launch_rows_int8(const RowsParams &p, cudaStream_t stream) {
     const int rows = threads >= 128 ? 1 : 128 / threads;
     if (threads > 1024) return cudaErrorInvalidValue;
     const Launch l = {dim3((p.rows + rows - 1) / rows), dim3(threads, rows), stream, lanes_log2};
-    if (v == 1) launch_v<1, 128>(p, l);
-    else if (v == 2 && threads <= 512) launch_v<2, 512>(p, l);
-    else if (v == 2) launch_v<2, 1024>(p, l);
-    else launch_v<4, 1024>(p, l);
-    return cudaGetLastError();
+    p.early = is_early(l.grid.x);
+    if (v == 1) return launch_v<1, 128>(p, l);
+    if (v == 2) return threads <= 512 ? launch_v<2, 512>(p, l) : launch_v<2, 1024>(p, l);
+    return launch_v<4, 1024>(p, l);
 }
 
 }  // namespace gdn

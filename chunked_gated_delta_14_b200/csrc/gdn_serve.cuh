@@ -20,6 +20,7 @@ struct PoolParams {
     const int32_t *cu_seqlens, *slots;
     float *state;
     void *o;
+    int early;          // set by the launcher: launched early
 };
 cudaError_t launch_recurrent_pool(const PoolParams &p, cudaStream_t stream);
 
@@ -34,6 +35,7 @@ struct RowsParams {
     void *residual_out;
     int8_t *q;
     float *scale;
+    int early;                           // set by the launcher: launched early
 };
 cudaError_t launch_rows_int8(const RowsParams &p, cudaStream_t stream);
 
@@ -54,6 +56,43 @@ struct PadRows {
     int rows;           // 0: none
 };
 cudaError_t launch_int8_pad_rows(const PadRows &x, const PadRows &w, int K, cudaStream_t stream);
+
+// A launch that may begin before the kernel ahead of it on the stream has ended (early): the
+// kernel sets itself up, then waits (grid_wait) for that one's end before it reads or writes
+// anything outside itself, in every thread, so that its own end comes after that one's.
+// Back to back from the host a product of 16 rows takes 5.6 us so, 8.2 without, and a norm
+// of 16 x 2048 on the device 1.85 instead of 2.1.  Grids of more blocks than run at once begin
+// after that end as ever: taking the places of the last blocks one by one they were spread
+// worse (long ragged sequences 588 us instead of 545), and the wait alone, in each of 8224
+// blocks, cost plain rows of 2048 1.4 of 8 us.
+inline bool is_early(unsigned blocks) { return blocks <= 296; }      // two an SM
+template <typename... A, typename... B>
+cudaError_t launch(bool early, void (*kernel)(A...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, unsigned cluster,
+                   B... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    cfg.attrs = attr;
+    if (early) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (cluster > 1) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        attr[cfg.numAttrs].val.clusterDim.x = cluster;
+        attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+        ++cfg.numAttrs;
+    }
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+#ifdef __CUDACC__
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// The kernel behind this one, if launched early, may begin once every block has said this.
+__device__ __forceinline__ void grid_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+#endif
 
 // Return (and clear) the error word of these kernels; the caller has synchronised.
 unsigned int pool_read_and_clear_error(cudaError_t *err);
