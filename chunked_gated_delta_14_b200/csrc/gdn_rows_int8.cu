@@ -121,13 +121,28 @@ __device__ __forceinline__ void store8(T *row, int i, int width, const F2 (&pair
             __stcs(reinterpret_cast<uint4 *>(row + i) + v, make_uint4(w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]));
         return;
     }
-    if (i + 8 <= width && (reinterpret_cast<uintptr_t>(row) & 3) == 0) {
-#pragma unroll
-        for (int k = 0; k < Words<T>::kCount; ++k) reinterpret_cast<uint32_t *>(row + i)[k] = w[k];
-    } else {
+    // the widest stores that the row's address allows (the same for all its threads)
+    constexpr int kW = Words<T>::kCount;
+    T *to = row + i;
+    const unsigned off = (unsigned)(reinterpret_cast<uintptr_t>(to) & 15);
+    if (i + 8 > width) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            if (i + e < width) put(row + i + e, x[e]);
+            if (i + e < width) put(to + e, x[e]);
+    } else if (off == 0) {
+#pragma unroll
+        for (int k = 0; k < kW; k += 4) reinterpret_cast<uint4 *>(to)[k / 4] = make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
+    } else if (off == 8) {
+#pragma unroll
+        for (int k = 0; k < kW; k += 2) reinterpret_cast<uint2 *>(to)[k / 2] = make_uint2(w[k], w[k + 1]);
+    } else if (off % 4 == 0) {
+#pragma unroll
+        for (int k = 0; k < kW; ++k) reinterpret_cast<uint32_t *>(to)[k] = w[k];
+    } else {                             // bf16 on 2 bytes: words of an odd number and the one behind it
+        put(to, x[0]);
+#pragma unroll
+        for (int k = 0; k + 1 < kW; ++k) reinterpret_cast<uint32_t *>(to + 1)[k] = __funnelshift_r(w[k], w[k + 1], 16);
+        put(to + 7, x[7]);
     }
 }
 
