@@ -388,7 +388,9 @@ GDN_API gdn_status gdn_chunk_fwd_static_scratch(const gdn_fwd_args *args, void *
  * arguments checked on the host before any launch, asynchronous on `stream`.
  * Calls with no rows (or sequences) return GDN_OK and launch nothing.  Strides
  * are in elements.  None of the calls keeps state or allocates.  They may be
- * captured into CUDA graphs. */
+ * captured into CUDA graphs.  Small grids are launched so that they may begin
+ * before the kernel ahead of them on the stream has ended (programmatic stream
+ * serialization); they wait for its end before they read or write. */
 
 /* Gated delta rule, token by token, on a pool of states:
  *

@@ -609,6 +609,42 @@ def test_the_same_call_twice_gives_the_same_bits():
     assert all(torch.equal(one, gdn.int8_matmul(x, xs, w, ws, out_dtype=F)) for _ in range(3))
 
 
+def test_small_calls_back_to_back_wait_for_one_another():
+    """Small launches begin before the one ahead has ended, and wait for it: the same bits as with
+    the device idle between calls, in place, with buffers that each call reads and the next writes."""
+    P, g = make_layer(37)
+    first = randn(g, 3, 512).to(BF), randn(g, 3, 512), 0.05 * randn(g, 3, 4, 128, 128)
+    wq, ws = gdn.quantize_int8(randn(g, 512, 511) / 512 ** 0.5)
+    wq = wq.contiguous()                                         # rows off 16 bytes: copied in each call
+
+    def run(wait):
+        hidden, residual, state = (t.clone() for t in first)
+        out, o = torch.empty(3, 512, device="cuda", dtype=BF), torch.empty(3, 4, 128, device="cuda", dtype=BF)
+        for i in range(60):
+            x, xs, _ = gdn.add_rms_norm_int8(hidden, P["norm"], residual, residual_out=residual)
+            wait()
+            row = gdn.int8_matmul(x, xs, *P["w_in"])
+            wait()
+            q, k, v, gate = (row[:, 512 * j:512 * (j + 1)].unflatten(1, (4, 128)) for j in range(4))
+            gdn.recurrent_fwd(q, k, v, None, None, state, qk_norm_eps=1e-6, out=o)
+            wait()
+            y, ys = gdn.gated_rms_norm_int8(o, gate, P["head"])
+            wait()
+            gdn.int8_matmul(y, ys, *P["w_out"], out=out)
+            wait()
+            z, zs = gdn.quantize_int8(out[:, :511])
+            wait()
+            gdn.int8_matmul(z, zs, wq, ws, out=hidden)           # what the next round's norm reads
+            wait()
+        return hidden, residual, state
+
+    want = run(torch.cuda.synchronize)
+    for _ in range(5):
+        assert all(torch.equal(a, b) for a, b in zip(run(lambda: None), want))
+    assert all(t.isfinite().all() for t in want)
+    gdn.device_check()
+
+
 def test_product_with_copies_captured_twice():
     """Two graphs of one stream, each with copies of unaligned rows: they share no workspace."""
     a, b = make_product(36, 30, 70, 333, pad=False), make_product(37, 50, 90, 555, pad=False)
