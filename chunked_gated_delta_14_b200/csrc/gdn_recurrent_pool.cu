@@ -579,14 +579,15 @@ __global__ void __launch_bounds__(W * 32, R < 16 ? 1 : LONG ? 8 / W : 12 / W) re
 }
 
 template <typename... A, typename... B>
-cudaError_t launch_blocks(void (*kernel)(PoolParams, A...), unsigned blocks, int threads, cudaStream_t stream, PoolParams p, B... args) {
-    p.early = is_early(blocks);
+cudaError_t launch_blocks(bool early, void (*kernel)(PoolParams, A...), unsigned blocks, int threads, cudaStream_t stream, PoolParams p,
+                          B... args) {
+    p.early = early;
     return launch(p.early, kernel, dim3(blocks), dim3(threads), 0, stream, 1, p, args...);
 }
 template <int R, bool BF16, int W>
 cudaError_t launch_ragged(const PoolParams &p, bool is_long, unsigned blocks, cudaStream_t stream) {
-    return launch_blocks(is_long ? recurrent_ragged_kernel<R, BF16, W, true, 1> : recurrent_ragged_kernel<R, BF16, W, false, 1>, blocks,
-                         W * 32, stream, p);
+    return launch_blocks(is_early(blocks), is_long ? recurrent_ragged_kernel<R, BF16, W, true, 1> : recurrent_ragged_kernel<R, BF16, W, false, 1>,
+                         blocks, W * 32, stream, p);
 }
 template <int R, bool BF16>
 cudaError_t launch_r(const PoolParams &p, cudaStream_t stream) {
@@ -598,7 +599,7 @@ cudaError_t launch_r(const PoolParams &p, cudaStream_t stream) {
         // Two column quads a lane where whole heads still fill the SMs twice (48 sequences x 32
         // heads 545 us, with one 648); fewer are quicker on more blocks.
         if (is_long && p.dv == 128 && blocks >= 296)
-            return launch_blocks(recurrent_ragged_kernel<R, BF16, 4, true, 2>, blocks, 128, stream, p);
+            return launch_blocks(is_early(blocks), recurrent_ragged_kernel<R, BF16, 4, true, 2>, blocks, 128, stream, p);
         if (p.dv % 64 == 0) return launch_ragged<R, BF16, 4>(p, is_long, blocks * (p.dv / 64), stream);
         return launch_ragged<R, BF16, 2>(p, is_long, blocks * (p.dv / 32), stream);
     }
@@ -606,7 +607,9 @@ cudaError_t launch_r(const PoolParams &p, cudaStream_t stream) {
     // where the heads are fewer than two a SM, 32, so that more SMs take part (16 heads: 2.8 us,
     // with 64 columns 3.2, with 128 4.2).
     const int slices = blocks < 296 ? p.dv / 32 : p.dv % 64 ? 1 : p.dv / 64, threads = p.dv / 4 / slices * kGroups;
-    return launch_blocks(p.vec ? recurrent_step_kernel<R, BF16, true> : recurrent_step_kernel<R, BF16, false>, blocks * slices, threads,
+    // Begun early at every size: equal blocks have no order to lose (32 x 16 heads 14.7 us, 15.5
+    // without; 128 x 32 heads 84.9, 85.8; 256 x 32 heads of 16 x 32 12.6, 13.0).
+    return launch_blocks(true, p.vec ? recurrent_step_kernel<R, BF16, true> : recurrent_step_kernel<R, BF16, false>, blocks * slices, threads,
                          stream, p, slices);
 }
 template <int R>
