@@ -270,6 +270,8 @@ __global__ void __launch_bounds__(W * 32, R < 16 ? 1 : LONG ? 8 / W : 12 / W) re
     constexpr int kMine = kBring / W;                // tokens of those a warp brings
     constexpr int kPer = (kDk + 31) / 32, kPerV = kWide / 32;   // numbers of k, v a lane brings
     constexpr int kDot = kThreads / (4 * kBring);    // threads that share a dot product
+    constexpr int kDotRounds = (kDk / 4 + kDot - 1) / kDot;     // fours of numbers each takes (d_k 16: some take none)
+    static_assert(kDotRounds >= 1 && kDotRounds * kDot >= kDk / 4, "every product is a whole row's");
     __shared__ __align__(16) float ks[3][kBring][kDk], qs[3][kBring][kDk], vs[3][kBring][kWide];
     __shared__ __align__(16) float alphas[3][kBring], betas[3][kBring], kk[2][kBring][kFour], kq[2][kBring][kFour];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slices = p.dv / kWide;
@@ -365,7 +367,8 @@ __global__ void __launch_bounds__(W * 32, R < 16 ? 1 : LONG ? 8 / W : 12 / W) re
         const float4 *y = reinterpret_cast<const float4 *>(ks[b][four + dot_j]) + part;
         float sum = 0.f;
 #pragma unroll
-        for (int m = 0; m < kDk / 4 / kDot; ++m) {
+        for (int m = 0; m < kDotRounds; ++m) {
+            if (kDk / 4 % kDot && part + m * kDot >= kDk / 4) break;
             const float4 u = x[m * kDot], v = y[m * kDot];
             sum = fmaf(u.x, v.x, fmaf(u.y, v.y, fmaf(u.z, v.z, fmaf(u.w, v.w, sum))));
         }

@@ -1,0 +1,44 @@
+"""Decode-layer operators on the GPU where their kernels change over: every head size in every
+variant, ties, the ends of the numbers' range, batches around a sequence, sizes near 2^31,
+overlapping rows, captures over two streams.
+
+Tolerances are those of test_layer_gpu.py, derived there beside each check.
+"""
+
+import pytest
+import torch
+
+import chunked_gated_delta_14_b200 as gdn
+from test_layer_gpu import BF, F, check_rule, make_rule, rule64
+
+pytestmark = pytest.mark.gpu
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def off16(x):
+    """The same numbers in rows and heads that start off 16 bytes."""
+    return torch.empty(x.shape[0], x.shape[1], x.shape[2] + 1, device="cuda", dtype=x.dtype)[..., 1:].copy_(x)
+
+
+# the variants that a batch's lengths choose: short sequences, long ones, long ones of whole heads by two column quads
+LENGTHS = {"short": [2, 3, 4, 5, 6, 7, 8, 9, 1, 0], "long": [40, 17, 2, 1, 33, 9, 0, 24, 23, 21],
+           "two quads": [40, 17, 2, 1, 33, 9, 0, 24, 23, 21] * 8}
+
+
+@pytest.mark.parametrize("io", [BF, F])
+@pytest.mark.parametrize("aligned", [True, False])
+@pytest.mark.parametrize("lengths,dk,dv", [(n, dk, dv) for n in LENGTHS for dk in (16, 32, 64, 128) for dv in (32, 64, 96, 128)
+                                           if n != "two quads" or dv == 128])
+def test_recurrent_every_size_in_every_variant(lengths, dk, dv, aligned, io):
+    lens = LENGTHS[lengths]
+    H = 4 if lengths == "two quads" else 2
+    q, k, v, al, be, state, starts = make_rule(70, lens, 2, H, dk, dv, io)
+    assert (lengths == "short") == (starts[-1] < 16 * len(lens))
+    S = range(len(lens))
+    want = rule64(q, k, v, al, be, state, S, starts, torch.zeros_like(v))
+    o = gdn.recurrent_fwd(*((q, k, v) if aligned else map(off16, (q, k, v))), al, be, state, None, i32(starts))
+    gdn.device_check()
+    check_rule(o, state, want, S, starts, q, dk, max(lens))
