@@ -276,12 +276,12 @@ int8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             const int acc = i & 1;
             const int row = quarter * 32 + lane, n = (PAIR ? 2 * tn + rank : tn) * g.channels + row, m0 = tm * BN;
             const bool has = row < g.channels && n < p.N;
-            const float ws = has ? __ldg(p.w_scale + n) : 0.f;
-            const float b = has && p.bias ? __ldg(p.bias + n) : 0.f;
+            const float ws = has ? plain(p.w_scale + n) : 0.f;
+            const float b = has && p.bias ? plain(p.bias + n) : 0.f;
             // the tokens' scales, a copy for each warp, while the sums are formed: the four warps have
             // no barrier among them that one which gives up could leave the others in
             __syncwarp();
-            for (int j = lane; j < BN; j += 32) x_scales[quarter][j] = m0 + j < p.M ? __ldg(p.x_scale + m0 + j) : 0.f;
+            for (int j = lane; j < BN; j += 32) x_scales[quarter][j] = m0 + j < p.M ? plain(p.x_scale + m0 + j) : 0.f;
             __syncwarp();
             if (!__all_sync(~0u, mbar_wait_cluster(&acc_full[acc], (i / 2) & 1, abort, 5, kLimit))) break;
             tc_fence_after();
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(256) pad_rows_kernel(const PadRows x, const Pa
         if (word >= reinterpret_cast<uintptr_t>(from) && word + 20 <= reinterpret_cast<uintptr_t>(from + K)) {
             uint32_t z[5];
 #pragma unroll
-            for (int j = 0; j < 5; ++j) z[j] = __ldg(reinterpret_cast<const uint32_t *>(word) + j);
+            for (int j = 0; j < 5; ++j) z[j] = plain(reinterpret_cast<const uint32_t *>(word) + j);
 #pragma unroll
             for (int j = 0; j < 4; ++j) y[j] = __funnelshift_r(z[j], z[j + 1], (uint32_t)(at & 3) * 8);
         } else {

@@ -42,23 +42,23 @@ struct Raw {
     __device__ __forceinline__ void load(const void *base, int64_t i) {
         const char *from = reinterpret_cast<const char *>(base) + i * (BF16 ? 2 : 4);
         if constexpr (BF16 && N == 1) {
-            w[0] = __ldg(reinterpret_cast<const uint16_t *>(from));
+            w[0] = plain(reinterpret_cast<const uint16_t *>(from));
         } else if constexpr (VEC && kWords % 4 == 0) {
 #pragma unroll
             for (int j = 0; j < kWords / 4; ++j) {
-                const uint4 x = __ldg(reinterpret_cast<const uint4 *>(from) + j);
+                const uint4 x = plain(reinterpret_cast<const uint4 *>(from) + j);
                 w[4 * j] = x.x; w[4 * j + 1] = x.y; w[4 * j + 2] = x.z; w[4 * j + 3] = x.w;
             }
         } else if constexpr (VEC && kWords == 2) {
-            const uint2 x = __ldg(reinterpret_cast<const uint2 *>(from));
+            const uint2 x = plain(reinterpret_cast<const uint2 *>(from));
             w[0] = x.x; w[1] = x.y;
         } else if constexpr (VEC || !BF16) {
 #pragma unroll
-            for (int j = 0; j < kWords; ++j) w[j] = __ldg(reinterpret_cast<const uint32_t *>(from) + j);
+            for (int j = 0; j < kWords; ++j) w[j] = plain(reinterpret_cast<const uint32_t *>(from) + j);
         } else {
             const uint16_t *x = reinterpret_cast<const uint16_t *>(from);
 #pragma unroll
-            for (int j = 0; j < N / 2; ++j) w[j] = (uint32_t)__ldg(x + 2 * j) | ((uint32_t)__ldg(x + 2 * j + 1) << 16);
+            for (int j = 0; j < N / 2; ++j) w[j] = (uint32_t)plain(x + 2 * j) | ((uint32_t)plain(x + 2 * j + 1) << 16);
         }
     }
     __device__ __forceinline__ float get(int r) const {
@@ -121,8 +121,8 @@ __device__ __forceinline__ void step(const PoolParams &p, int slot, int64_t t, i
     float v[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) v[c] = load1(p.v, t * p.v_row + (int64_t)h * p.v_head + col + c, BF16);
-    const float a = p.alpha ? __ldg(p.alpha + t * p.alpha_row + h) : 1.f;
-    const float be = p.beta ? __ldg(p.beta + t * p.beta_row + h) : 1.f;
+    const float a = p.alpha ? plain(p.alpha + t * p.alpha_row + h) : 1.f;
+    const float be = p.beta ? plain(p.beta + t * p.beta_row + h) : 1.f;
 
     float4 hk4 = make_float4(0.f, 0.f, 0.f, 0.f), hq4 = hk4;
     float kk = 0.f, qq = 0.f, kq = 0.f;
@@ -325,8 +325,8 @@ __global__ void __launch_bounds__(W * 32, R < 16 ? 1 : LONG ? 8 / W : 12 / W) re
                 }
                 if (p.vec) vr[m].template load<true>(p.v, t * p.v_row + vo);
                 else vr[m].template load<false>(p.v, t * p.v_row + vo);
-                if (p.alpha) ar[m] = __ldg(p.alpha + t * p.alpha_row + h);
-                if (p.beta) br[m] = __ldg(p.beta + t * p.beta_row + h);
+                if (p.alpha) ar[m] = plain(p.alpha + t * p.alpha_row + h);
+                if (p.beta) br[m] = plain(p.beta + t * p.beta_row + h);
             }
         }
     };

@@ -71,7 +71,7 @@ __device__ __forceinline__ void load8(const T *row, int i, int width, uint32_t (
 #pragma unroll
         for (int v = 0; v < kW / 4 + 1; ++v) {
             uint4 z = make_uint4(0, 0, 0, 0);
-            if (v < kW / 4 || off) z = __ldg(reinterpret_cast<const uint4 *>(from) + v);
+            if (v < kW / 4 || off) z = plain(reinterpret_cast<const uint4 *>(from) + v);
             y[4 * v] = z.x; y[4 * v + 1] = z.y; y[4 * v + 2] = z.z; y[4 * v + 3] = z.w;
         }
         if (off & 8) {
@@ -152,7 +152,7 @@ __device__ __forceinline__ void weight8(const T *weight, int i, int width, bool 
     if (VEC || (vec && i + 8 <= width)) {
 #pragma unroll
         for (int v = 0; v < Words<T>::kCount / 4; ++v) {
-            const uint4 y = __ldg(reinterpret_cast<const uint4 *>(weight + i) + v);
+            const uint4 y = plain(reinterpret_cast<const uint4 *>(weight + i) + v);
             w[4 * v] = y.x; w[4 * v + 1] = y.y; w[4 * v + 2] = y.z; w[4 * v + 3] = y.w;
         }
     } else {

@@ -89,6 +89,11 @@ cudaError_t launch(bool early, void (*kernel)(A...), dim3 grid, dim3 block, size
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 #ifdef __CUDACC__
+// How these kernels read their operands: an ordinary load.  The read-only path (__ldg) is for
+// data that nothing writes while the kernel lives, and one launched early lives while the
+// kernel ahead still writes what it is going to read behind the wait.
+template <typename T>
+__device__ __forceinline__ T plain(const T *p) { return *p; }
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // The kernel behind this one, if launched early, may begin once every block has said this.
 __device__ __forceinline__ void grid_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
