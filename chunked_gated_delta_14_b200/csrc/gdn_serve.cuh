@@ -28,6 +28,7 @@ struct RowsParams {
     int op, rows, width, head;
     int x_bf16, residual_bf16, weight_bf16;
     int vec;                             // every row starts on 16 bytes, width a multiple of 8
+    int in_place;                        // residual_out is x or the residual
     int weight_vec, q_vec;               // the weight starts on 16 bytes, every row of q on 8
     float eps, inverse;                  // inverse: 1 / the numbers a norm is of
     const void *x, *residual, *gate, *weight;

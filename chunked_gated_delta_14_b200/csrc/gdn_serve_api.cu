@@ -136,6 +136,7 @@ gdn_status resolve_rows(const gdn_rows_args *a, gdn::RowsParams *out) {
     p.residual_out_row = a->residual_out_row; p.q_row = a->q_row;
     p.residual_out = a->residual_out; p.q = a->q; p.scale = a->scale;
     const auto rows16 = [](const void *ptr, int64_t row, int64_t size) { return !ptr || (on16(ptr) && row * size % 16 == 0); };
+    p.in_place = a->residual_out && (a->residual_out == a->residual || a->residual_out == a->x);
     p.weight_vec = on16(a->weight);
     p.q_vec = on(a->q, 8) && (a->q_row % 8 == 0 || a->rows == 1);
     p.vec = a->width % 8 == 0 && rows16(a->x, a->x_row, xs) && rows16(a->residual, a->residual_row, rs) &&

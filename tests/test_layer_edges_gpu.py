@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import chunked_gated_delta_14_b200 as gdn
-from test_layer_gpu import BF, F, check_rule, make_rule, rule64
+from test_layer_gpu import BF, F, check_rule, make_rule, randn, rng, rule64
 
 pytestmark = pytest.mark.gpu
 
@@ -42,3 +42,20 @@ def test_recurrent_every_size_in_every_variant(lengths, dk, dv, aligned, io):
     o = gdn.recurrent_fwd(*((q, k, v) if aligned else map(off16, (q, k, v))), al, be, state, None, i32(starts))
     gdn.device_check()
     check_rule(o, state, want, S, starts, q, dk, max(lens))
+
+
+@pytest.mark.parametrize("io", [BF, F])
+@pytest.mark.parametrize("D,pitch,off", [(1001, 1001, 0), (77, 79, 1), (2049, 2051, 3), (16001, 16001, 0), (2048, 2049, 1)])
+def test_norm_in_place_of_rows_off_16_bytes(D, pitch, off, io):
+    """The pieces that a thread reads hold numbers that its neighbours overwrite."""
+    g = rng(82)
+    make = lambda: randn(g, 300 * pitch + off).to(io)[off:].view(300, pitch)[:, :D]  # noqa: E731
+    x, r = make(), make()
+    want = gdn.add_rms_norm_int8(x.clone(), None, r.clone())
+    for place in (r, x):
+        keep = place.clone()
+        for _ in range(3):
+            place.copy_(keep)
+            got = gdn.add_rms_norm_int8(x, None, r, residual_out=place)
+            assert got[2] is place and all(torch.equal(a, b) for a, b in zip(got, want))
+        place.copy_(keep)
