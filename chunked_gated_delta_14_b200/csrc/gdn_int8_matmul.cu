@@ -290,6 +290,7 @@ int8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
 #pragma unroll 1
             for (int c = 0; c < BN; c += kCols) {
                 if (m0 + c >= p.M || quarter * 32 >= g.channels) break;
+                __syncwarp();            // the loads below are the whole warp's, also behind a store of some lanes
                 uint32_t r[kCols];
                 if constexpr (kCols == 16) tmem_ld16(taddr + c, r);
                 else tmem_ld32(taddr + c, r);
@@ -297,14 +298,15 @@ int8_matmul_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                 const int left = min(kCols, p.M - m0 - c);
                 const int64_t o = (int64_t)(m0 + c) * p.out_row + n;
                 const float *xs = &x_scales[quarter][c];
-                if (!has) continue;
-                if (left == kCols) {
-                    if (p.out_bf16) store_column<kCols>(reinterpret_cast<__nv_bfloat16 *>(p.out) + o, p.out_row, r, xs, ws, b);
-                    else store_column<kCols>(reinterpret_cast<float *>(p.out) + o, p.out_row, r, xs, ws, b);
-                } else {
+                if (has) {
+                    if (left == kCols) {
+                        if (p.out_bf16) store_column<kCols>(reinterpret_cast<__nv_bfloat16 *>(p.out) + o, p.out_row, r, xs, ws, b);
+                        else store_column<kCols>(reinterpret_cast<float *>(p.out) + o, p.out_row, r, xs, ws, b);
+                    } else {
 #pragma unroll
-                    for (int j = 0; j < kCols; ++j)
-                        if (j < left) store_one(p, o + j * p.out_row, (int)r[j], xs[j], ws, b);
+                        for (int j = 0; j < kCols; ++j)
+                            if (j < left) store_one(p, o + j * p.out_row, (int)r[j], xs[j], ws, b);
+                    }
                 }
             }
             tc_fence_before();

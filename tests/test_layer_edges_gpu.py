@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import chunked_gated_delta_14_b200 as gdn
-from test_layer_gpu import BF, F, check_rule, make_rule, randn, rng, rule64
+from test_layer_gpu import BF, F, check_product, check_rule, make_product, make_rule, randn, rng, rule64
 
 pytestmark = pytest.mark.gpu
 
@@ -59,3 +59,17 @@ def test_norm_in_place_of_rows_off_16_bytes(D, pitch, off, io):
             got = gdn.add_rms_norm_int8(x, None, r, residual_out=place)
             assert got[2] is place and all(torch.equal(a, b) for a, b in zip(got, want))
         place.copy_(keep)
+
+
+@pytest.mark.parametrize("out_dtype", [BF, F])
+@pytest.mark.parametrize("M,N,K", [(40, 7, 64), (64, 17, 4096), (130, 9, 130), (200, 2001, 512), (128, 2008, 128), (100, 1001, 2048),
+                                   (257, 8221, 256), (1030, 4099, 640), (500, 33, 100), (2100, 2050, 128)])
+def test_product_of_channels_that_end_inside_a_warp(M, N, K, out_dtype):
+    """Several loads of the accumulator behind stores of some lanes, in tiles of every kind; what
+    lies behind the channels is left as it was."""
+    x, xs, w, ws, bias = make_product(83, M, N, K, bias=True)
+    out = torch.full((M + 1, N + 3), 7.0, device="cuda", dtype=out_dtype)
+    gdn.int8_matmul(x, xs, w, ws, bias, out_dtype=out_dtype, out=out[:M, :N])
+    gdn.device_check()
+    check_product(out[:M, :N], x, xs, w, ws, bias)
+    assert (out[M] == 7).all() and (out[:, N:] == 7).all()
