@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(W * 32, R < 16 ? 1 : LONG ? 8 / W : 12 / W) re
                 for (int c = 0; c < 4; ++c) g[z][r][c] = mul2(g[z][r][c], f);
     };
 
-    const int brings = (end - begin + kBring - 1) / kBring;
+    const int brings = (end - begin - 1) / kBring + 1;
     fetch(0);                            // before the state: it is needed first
     float4 rows[NQ][R];
 #pragma unroll

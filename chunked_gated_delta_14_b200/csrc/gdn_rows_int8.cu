@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(MOST) rows_kernel(const RowsParams p) {
     if (p.early) { grid_next(); grid_wait(); }
     constexpr bool RES = !std::is_void<RT>::value;
     using R1 = typename std::conditional<RES, RT, float>::type;
-    const int row = blockIdx.x * blockDim.y + threadIdx.y;
+    const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;      // (past 2^31 in the last block of as many)
     const int width = row < p.rows ? p.width : 0;
     const int64_t r = row < p.rows ? row : 0;
     const XT *x = reinterpret_cast<const XT *>(p.x) + r * p.x_row;
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(MOST) rows_kernel(const RowsParams p) {
 template <typename XT, int V, int MOST, bool VEC>
 __global__ void __launch_bounds__(MOST) gated_kernel(const RowsParams p, int lanes_log2, int heads) {
     if (p.early) { grid_next(); grid_wait(); }
-    const int row = blockIdx.x * blockDim.y + threadIdx.y;
+    const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
     const bool on = row < p.rows;
     const int64_t r = on ? row : 0;
     const XT *x = reinterpret_cast<const XT *>(p.x) + r * p.x_row;
@@ -468,7 +468,7 @@ cudaError_t launch_rows_int8(const RowsParams &given, cudaStream_t stream) {
     const int threads = ((need + v - 1) / v + 31) / 32 * 32;
     const int rows = threads >= 128 ? 1 : 128 / threads;
     if (threads > 1024) return cudaErrorInvalidValue;
-    const Launch l = {dim3((p.rows + rows - 1) / rows), dim3(threads, rows), stream, lanes_log2};
+    const Launch l = {dim3(((unsigned)p.rows + rows - 1) / rows), dim3(threads, rows), stream, lanes_log2};
     p.early = is_early(l.grid.x);
     if (v == 1) return launch_v<1, 128>(p, l);
     if (v == 2) return threads <= 512 ? launch_v<2, 512>(p, l) : launch_v<2, 1024>(p, l);

@@ -73,3 +73,13 @@ def test_product_of_channels_that_end_inside_a_warp(M, N, K, out_dtype):
     gdn.device_check()
     check_product(out[:M, :N], x, xs, w, ws, bias)
     assert (out[M] == 7).all() and (out[:, N:] == 7).all()
+
+
+def test_rows_as_many_as_the_arguments_hold():
+    """2^31 - 1 rows, in blocks of four: the last block's rows pass 2^31."""
+    R = 2 ** 31 - 1
+    q, scale = gdn.quantize_int8(torch.full((1, 1), -3.0, device="cuda").expand(R, 1))
+    assert q.shape == (R, 1) and (q == -127).all()
+    assert (scale == scale[0]).all() and scale[0] == 3.0 / 127
+    del q, scale
+    torch.cuda.empty_cache()
