@@ -178,17 +178,25 @@ __device__ __forceinline__ float rcp(float x) {
     return y;
 }
 
-// The row's scale, and the factor from y to steps (0 where the row has none).
-__device__ __forceinline__ float scale_of(float top, float *factor) {
-    *factor = 0.f;
-    if (!(top < __uint_as_float(kInfBits))) return __uint_as_float(0x7fc00000u);
-    const float s = top * (1.f / 127.f);
-    if (s < 1.17549435e-38f) return 0.f;
-    // 127 / top, one correction after an approximate reciprocal; with a sixteenth of both, which
-    // keeps the reciprocal normal for tops from 1.5e-36 to 3.4e38
-    const float t = top * 0.0625f, r = rcp(t), f = 7.9375f * r;
-    *factor = fmaf(fmaf(-f, t, 7.9375f), r, f);
-    return s;
+constexpr float kLeast = 127 * 0x1p-126f;            // the largest of a row with the least scale
+__device__ __forceinline__ bool fits(float x) { return x < __uint_as_float(kInfBits); }
+
+// Quotients, by Markstein's correction q + (a - q b) r of an approximate one, with r about 1 / b
+// ("Computation of elementary functions on the IBM RISC System/6000 processor", 1990): three
+// instructions, where a division by its operator cost plain rows of 8192 x 8192 5 us of 32.
+//
+// The row's scale, top / 127: r is 1 / 127 rounded correctly, so the quotient is too.
+__device__ __forceinline__ float scale_of(float top) {
+    if (!fits(top)) return __uint_as_float(0x7fc00000u);
+    const float r = 1.f / 127.f, q = top * r;
+    return top < kLeast ? 0.f : fmaf(fmaf(-q, 127.f, top), r, q);
+}
+// The factor from numbers to steps, 127 / top (0 where the row has none); with a sixteenth of
+// both, which keeps the reciprocal normal for tops from kLeast to 3.4e38.
+__device__ __forceinline__ float steps_of(float top) {
+    if (!(top >= kLeast) || !fits(top)) return 0.f;
+    const float t = top * 0.0625f, r = rcp(t), q = 7.9375f * r;
+    return fmaf(fmaf(-q, t, 7.9375f), r, q);
 }
 
 // Steps of 8 numbers.  y f + 1.5 2^23 has rint(y f) in its low bits (|y f| <= 127 and a
@@ -240,6 +248,18 @@ __device__ __forceinline__ void times(F2 (&x)[4], float y) {
     for (int e = 0; e < 4; ++e) x[e] = mul2(x[e], pack(y, y));
 }
 
+// Squares of numbers from about 2^62 on leave fp32 in a row's sum.  Beside each sum of squares
+// goes the sum of the squares of 2^-72 h, which holds any row (2^15 squares below 2^112) and is
+// read only where the first is infinite: it is then at least 2^-16, and what the multiple below
+// 2^-126 loses does not count.
+constexpr float kSmall = 0x1p-72f, kSmall2 = 0x1p-144f;
+__device__ __forceinline__ float small_squares(const F2 (&x)[4]) {
+    F2 y[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = mul2(x[e], pack(kSmall, kSmall));
+    return squares(y);
+}
+
 // Sum and largest over the row's threads (blockDim.x of them, whole warps).  As whole
 // numbers, values from 0 up order like themselves, with NaN above infinity.
 struct Totals { float sum, top; };
@@ -266,6 +286,22 @@ __device__ __forceinline__ Totals row_totals(float sum, float top_value) {
         for (int m = 16; m; m /= 2) sum += __shfl_xor_sync(~0u, sum, m);
     }
     return {sum, __uint_as_float(top)};
+}
+
+// The sum alone, for a row whose sum of squares does not fit: its warps meet at a barrier of
+// their own (the block's other rows may not come here).
+__device__ __forceinline__ float row_sum(float sum) {
+    __shared__ float sums[32];
+#pragma unroll
+    for (int m = 16; m; m /= 2) sum += __shfl_xor_sync(~0u, sum, m);
+    const int warps = blockDim.x >> 5, first = threadIdx.y * warps, lane = threadIdx.x & 31;
+    if (warps == 1) return sum;
+    if (lane == 0) sums[first + (threadIdx.x >> 5)] = sum;
+    sm100::named_bar(1 + threadIdx.y, blockDim.x);
+    sum = lane < warps ? sums[first + lane] : 0.f;
+#pragma unroll
+    for (int m = 16; m; m /= 2) sum += __shfl_xor_sync(~0u, sum, m);
+    return sum;
 }
 
 // PLAIN and NORM.  XT: type of x.  RT: type of the residual, or void for none.
@@ -296,7 +332,7 @@ __global__ void __launch_bounds__(MOST) rows_kernel(const RowsParams p) {
     // all of a row's loads come before its stores (4096 x 5001 in place 52.8 us, 48.0 without)
     if (RES && !VEC && p.in_place) __syncthreads();
     F2 h[V][4];
-    float sum = 0.f, top = 0.f;
+    float sum = 0.f, small = 0.f, top = 0.f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         widen<XT>(xw[j], h[j]);
@@ -308,29 +344,46 @@ __global__ void __launch_bounds__(MOST) rows_kernel(const RowsParams p) {
             if (at(j) < width)
                 store8<VEC>(reinterpret_cast<R1 *>(p.residual_out) + r * p.residual_out_row, at(j), width, h[j]);
         }
-        if constexpr (NORM) {
-            sum += squares(h[j]);
-            if (p.weight) {
-                F2 w[4];
-                widen<WT>(ww[j], w);
-                times(h[j], w);
-            }
+        if (NORM) sum += squares(h[j]);
+    }
+    if constexpr (NORM) {
+        small = sum * kSmall2;
+        if (!fits(sum)) {
+            small = 0.f;
+#pragma unroll
+            for (int j = 0; j < V; ++j) small += small_squares(h[j]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        if (NORM && p.weight) {
+            F2 w[4];
+            widen<WT>(ww[j], w);
+            times(h[j], w);
         }
         top = top_of(top, h[j]);
     }
     const Totals t = row_totals<NORM>(sum, top);
     if (!width) return;
-    float f, norm = 1.f;
-    if constexpr (NORM) norm = rsqrtf(fmaf(t.sum, p.inverse, p.eps));
-    const float scale = scale_of(t.top * norm, &f);
-    if (threadIdx.x == 0) p.scale[r] = scale;
-    // y f = (h w) (norm f); where that factor is out of range (h w far below the normal
-    // numbers, and the norm lifts it back) the norm goes into h w first
-    if (f == 0.f) clear(h);
-    else if (NORM && f * norm < __uint_as_float(kInfBits)) f *= norm;
-    else if (NORM)
+    // y f = (h w) 127 / max|h w|: the norm's factor is the whole row's.  It makes the largest y
+    // of the largest h w.
+    float f = steps_of(t.top), most = t.top;
+    if constexpr (NORM) {
+        float norm = rsqrtf(fmaf(t.sum, p.inverse, p.eps));
+        most *= norm;
+        if (!fits(t.sum)) {              // (of a row that is not finite too: NaN, or infinity times 0)
+            norm = rsqrtf(fmaf(row_sum(small), p.inverse, p.eps * kSmall2));
+            most = t.top * 0x1p-36f * norm * 0x1p-36f;
+        }
+        if (t.top < kLeast) {            // h w far below the normal numbers: the norm may lift it back
+            f = steps_of(most);
 #pragma unroll
-        for (int j = 0; j < V; ++j) times(h[j], norm);
+            for (int j = 0; j < V; ++j) times(h[j], norm);
+        }
+        if (!(most >= kLeast) || !fits(most)) f = 0.f;
+    }
+    if (threadIdx.x == 0) p.scale[r] = scale_of(most);
+    if (f == 0.f) clear(h);
     int8_t *q = p.q + r * p.q_row;
 #pragma unroll
     for (int j = 0; j < V; ++j)
@@ -386,9 +439,26 @@ __global__ void __launch_bounds__(MOST) gated_kernel(const RowsParams p, int lan
         if (m < lanes)
 #pragma unroll
             for (int j = 0; j < V; ++j) norm[j] += __shfl_xor_sync(~0u, norm[j], m);
+    float all = norm[0];
+#pragma unroll
+    for (int j = 1; j < V; ++j) all += norm[j];
+    if (__any_sync(~0u, !fits(all))) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            float small = small_squares(y[j]);
+#pragma unroll
+            for (int m = 16; m; m /= 2)
+                if (m < lanes) small += __shfl_xor_sync(~0u, small, m);
+            const bool big = !fits(norm[j]);
+            norm[j] = big ? rsqrtf(fmaf(small, p.inverse, p.eps * kSmall2)) : rsqrtf(fmaf(norm[j], p.inverse, p.eps));
+            if (big) times(y[j], kSmall);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) norm[j] = rsqrtf(fmaf(norm[j], p.inverse, p.eps));
+    }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const float n = rsqrtf(fmaf(norm[j], p.inverse, p.eps));
         F2 gate[4];
         widen<XT>(gw[j], gate);
         // g / (1 + e^-g): an approximate exponential and quotient, off by some 2^-22 of the
@@ -400,16 +470,15 @@ __global__ void __launch_bounds__(MOST) gated_kernel(const RowsParams p, int lan
             unpack(add2(pack(sm100::ex2_approx(lo), sm100::ex2_approx(hi)), pack(1.f, 1.f)), &lo, &hi);
             gate[e] = mul2(gate[e], pack(rcp(lo), rcp(hi)));
         }
-        times(y[j], n);
+        times(y[j], norm[j]);
         times(y[j], w);
         times(y[j], gate);
         top = top_of(top, y[j]);
     }
     const Totals t = row_totals<false>(0.f, top);
     if (!on) return;
-    float f;
-    const float scale = scale_of(t.top, &f);
-    if (threadIdx.x == 0) p.scale[r] = scale;
+    if (threadIdx.x == 0) p.scale[r] = scale_of(t.top);
+    const float f = steps_of(t.top);
     if (f == 0.f) clear(y);
     int8_t *q = p.q + r * p.q_row;
 #pragma unroll

@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import chunked_gated_delta_14_b200 as gdn
-from test_layer_gpu import BF, F, check_product, check_rule, make_product, make_rule, randn, rng, rule64
+from test_layer_gpu import BF, F, check_product, check_rows, check_rule, make_product, make_rule, randn, rng, rows_x, rule64
 
 pytestmark = pytest.mark.gpu
 
@@ -83,3 +83,50 @@ def test_rows_as_many_as_the_arguments_hold():
     assert (scale == scale[0]).all() and scale[0] == 3.0 / 127
     del q, scale
     torch.cuda.empty_cache()
+
+
+BIG = [1e18, 1e19, 1e25, 1e30, 1e38, 3e38]
+
+
+@pytest.mark.parametrize("io", [BF, F])
+@pytest.mark.parametrize("res", [None, BF, F])
+@pytest.mark.parametrize("D", [8, 64, 300, 1001, 2048, 8192, 20001])
+def test_norm_of_rows_whose_squares_pass_32_bits(D, res, io):
+    x = rows_x(74, (len(BIG) + 2, D), F)
+    x *= torch.tensor(BIG + [1.0, 1e20], device="cuda")[:, None] / x.abs().amax(1, keepdim=True)
+    x[len(BIG) + 1, 1:] *= 1e-15
+    x = x.to(io)
+    r = None if res is None else (x.float() * -0.25).to(res)
+    w = 1 + 0.2 * randn(rng(75), D)
+    w /= w.abs().max()            # |h w| stays in range where |h| does
+    q, scale, h = gdn.add_rms_norm_int8(x, w, r)
+    full = (x.float() if r is None else x.float() + r.float()).double()
+    assert full.abs().max() < 3.3e38
+    check_rows(q, scale, full / (full.pow(2).mean(-1, keepdim=True) + 1e-6).sqrt() * w.double())
+
+
+def test_norm_of_rows_past_the_range_have_scale_nan():
+    x = torch.full((2, 64), 3e38, device="cuda")
+    q, scale, _ = gdn.add_rms_norm_int8(x, torch.full((64,), 2.0, device="cuda"))
+    assert scale.isnan().all() and not q.any()
+    q, scale, h = gdn.add_rms_norm_int8(x, None, x)
+    assert scale.isnan().all() and not q.any() and h.isinf().all()
+    x = torch.zeros(2, 64, device="cuda")
+    x[:, 5] = 1.0                                    # y = 8 w there
+    q, scale, _ = gdn.add_rms_norm_int8(x, torch.full((64,), 1e38, device="cuda"))
+    assert scale.isnan().all() and not q.any()
+
+
+@pytest.mark.parametrize("io", [BF, F])
+@pytest.mark.parametrize("H,d", [(1, 8), (3, 40), (16, 128), (5, 96), (128, 256)])
+def test_gated_of_heads_whose_squares_pass_32_bits(H, d, io):
+    g = rng(76)
+    x = randn(g, len(BIG) + 1, H, d)
+    x *= torch.tensor(BIG + [1.0], device="cuda")[:, None, None] / x.abs().amax((1, 2), keepdim=True)
+    if H > 1:
+        x[:, 1] *= 1e-17
+    x, gate, w = x.to(io), randn(g, len(BIG) + 1, H, d).to(io), 1 + 0.2 * randn(g, d)
+    q, scale = gdn.gated_rms_norm_int8(x, gate, w)
+    xd, gd = x.double(), gate.double()
+    y = xd / (xd.pow(2).mean(-1, keepdim=True) + 1e-6).sqrt() * w.double() * gd * torch.sigmoid(gd)
+    check_rows(q, scale, y.flatten(1))
