@@ -191,26 +191,35 @@ __device__ __forceinline__ float scale_of(float top) {
     const float r = 1.f / 127.f, q = top * r;
     return top < kLeast ? 0.f : fmaf(fmaf(-q, 127.f, top), r, q);
 }
-// The factor from numbers to steps, 127 / top (0 where the row has none); with a sixteenth of
-// both, which keeps the reciprocal normal for tops from kLeast to 3.4e38.
-__device__ __forceinline__ float steps_of(float top) {
-    if (!(top >= kLeast) || !fits(top)) return 0.f;
+// The factor from numbers to steps, 127 / top rounded up (0 where the row has none), and what it
+// is more than the quotient; with a sixteenth of both, which keeps the reciprocal normal for tops
+// from kLeast to 3.4e38.
+struct Factor { float f, over; };
+__device__ __forceinline__ Factor steps_of(float top) {
+    if (!(top >= kLeast) || !fits(top)) return {0.f, 0.f};
     const float t = top * 0.0625f, r = rcp(t), q = 7.9375f * r;
-    return fmaf(fmaf(-q, t, 7.9375f), r, q);
+    float f = fmaf(fmaf(-q, t, 7.9375f), r, q);
+    if (fmaf(-f, t, 7.9375f) > 0.f) f = __uint_as_float(__float_as_uint(f) + 1);
+    return {f, fmaf(f, t, -7.9375f) * r};
 }
 
-// Steps of 8 numbers.  y f + 1.5 2^23 has rint(y f) in its low bits (|y f| <= 127 and a
-// rounding): a sum in place of a conversion, which has a quarter of the rate.  The product is
-// rounded first: of a row's bf16 numbers many are half the largest, 63.5 steps, and the
-// rounding puts the product back on that tie where f is a little off.
-template <bool VEC>
-__device__ __forceinline__ void store_steps8(int8_t *row, int i, int width, const F2 (&y)[4], float f, bool on8) {
+// Steps of 8 numbers.  y f + 1.5 2^23 has rint(y f) in its low bits (|y f| <= 127 and little
+// more): a sum in place of a conversion, which has a quarter of the rate, and one rounding for
+// both.  In a row of bf16 the numbers of half the largest are ties, 63.5 steps, which go to 64:
+// so they do with an f that is the quotient or above it, and no other number of such a row is
+// so close to a tie that an f off by two units moves it (tried for every pair of significands;
+// rounded to nearest, f took one tie in twelve to 63).
+// EXACT, for rows of fp32, whose bytes leave the time for it: y (f - over), rounded, and then to a
+// whole number.
+template <bool VEC, bool EXACT>
+__device__ __forceinline__ void store_steps8(int8_t *row, int i, int width, const F2 (&y)[4], Factor f, bool on8) {
     uint32_t b[8];
-    const F2 ff = pack(f, f), magic = pack(12582912.f, 12582912.f);
+    const F2 ff = pack(f.f, f.f), over = pack(-f.over, -f.over), magic = pack(12582912.f, 12582912.f);
 #pragma unroll
     for (int e = 0; e < 8; e += 2) {
         float lo, hi;
-        unpack(add2(mul2(y[e / 2], ff), magic), &lo, &hi);
+        if constexpr (EXACT) unpack(add2(fma2(y[e / 2], ff, mul2(y[e / 2], over)), magic), &lo, &hi);
+        else unpack(fma2(y[e / 2], ff, magic), &lo, &hi);
         b[e] = __float_as_uint(lo);
         b[e + 1] = __float_as_uint(hi);
     }
@@ -367,7 +376,8 @@ __global__ void __launch_bounds__(MOST) rows_kernel(const RowsParams p) {
     if (!width) return;
     // y f = (h w) 127 / max|h w|: the norm's factor is the whole row's.  It makes the largest y
     // of the largest h w.
-    float f = steps_of(t.top), most = t.top;
+    Factor f = steps_of(t.top);
+    float most = t.top;
     if constexpr (NORM) {
         float norm = rsqrtf(fmaf(t.sum, p.inverse, p.eps));
         most *= norm;
@@ -380,14 +390,14 @@ __global__ void __launch_bounds__(MOST) rows_kernel(const RowsParams p) {
 #pragma unroll
             for (int j = 0; j < V; ++j) times(h[j], norm);
         }
-        if (!(most >= kLeast) || !fits(most)) f = 0.f;
+        if (!(most >= kLeast) || !fits(most)) f.f = 0.f;
     }
     if (threadIdx.x == 0) p.scale[r] = scale_of(most);
-    if (f == 0.f) clear(h);
+    if (f.f == 0.f) clear(h);
     int8_t *q = p.q + r * p.q_row;
 #pragma unroll
     for (int j = 0; j < V; ++j)
-        if (at(j) < width) store_steps8<VEC>(q, at(j), width, h[j], f, p.q_vec);
+        if (at(j) < width) store_steps8<VEC, !NORM && sizeof(XT) == 4>(q, at(j), width, h[j], f, p.q_vec);
 }
 
 // GATED.  `lanes` (a power of two, 8 channels each) threads take a head, idle
@@ -478,12 +488,12 @@ __global__ void __launch_bounds__(MOST) gated_kernel(const RowsParams p, int lan
     const Totals t = row_totals<false>(0.f, top);
     if (!on) return;
     if (threadIdx.x == 0) p.scale[r] = scale_of(t.top);
-    const float f = steps_of(t.top);
-    if (f == 0.f) clear(y);
+    const Factor f = steps_of(t.top);
+    if (f.f == 0.f) clear(y);
     int8_t *q = p.q + r * p.q_row;
 #pragma unroll
     for (int j = 0; j < V; ++j)
-        if (has(j)) store_steps8<VEC>(q, at(j), p.width, y[j], f, p.q_vec);
+        if (has(j)) store_steps8<VEC, false>(q, at(j), p.width, y[j], f, p.q_vec);
 }
 
 struct Launch {

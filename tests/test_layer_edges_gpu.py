@@ -130,3 +130,38 @@ def test_gated_of_heads_whose_squares_pass_32_bits(H, d, io):
     xd, gd = x.double(), gate.double()
     y = xd / (xd.pow(2).mean(-1, keepdim=True) + 1e-6).sqrt() * w.double() * gd * torch.sigmoid(gd)
     check_rows(q, scale, y.flatten(1))
+
+
+@pytest.mark.parametrize("width", [64, 1001, 2048, 9000])
+def test_quantize_rounds_ties_to_even(width):
+    """Of rows in bf16 many numbers are a tie (half the row's largest is 63.5 steps): each step is
+    the definition's, rint(127 y / top).  In 64 bits 127 y is exact and so is a quotient that is a tie."""
+    g = rng(73)
+    R = 1024
+    top = (1 + torch.arange(R, device="cuda") % 128 / 128) * 2.0 ** (torch.arange(R, device="cuda") // 128 * 30 - 100)
+    x = (2 * torch.rand(R, width, device="cuda", generator=g) - 1) * top[:, None]
+    x[:, 1::3] = top[:, None] / 2 ** torch.randint(0, 8, (R, width), device="cuda", generator=g)[:, 1::3]
+    x = x.to(BF)
+    x[:, 0], x[:, width // 2] = top.to(BF), -top.to(BF) / 2
+    q, scale = gdn.quantize_int8(x)
+    y = x.double()
+    t = y.abs().amax(1, keepdim=True)
+    want = (127 * y / t).round()
+    assert torch.equal(q.double(), want)
+    assert torch.equal(scale, (t[:, 0] / 127).float())           # rounded correctly: the quotient in 64 bits is far from a tie
+    q, scale, _ = gdn.add_rms_norm_int8(x[512:])                  # the same ratios, and so the same steps
+    assert torch.equal(q.double(), want[512:])
+
+
+def test_quantize_of_fp32_takes_the_nearest_step():
+    """y (f - over): the product's rounding and the sum's, 2^-18 of a step and half a step; ties as they are."""
+    g = rng(86)
+    x = randn(g, 2000, 1001)
+    x[:, 7] = x.abs().amax(1) / 2
+    q, scale = gdn.quantize_int8(x)
+    t = x.double().abs().amax(1, keepdim=True)
+    y = 127 * x.double() / t
+    assert ((q.double() - y).abs() <= 0.5 + 2 ** -18).all()
+    half = y[:, 7] == 63.5                                        # not where column 7 was the largest itself
+    assert half.sum() > 1900 and (q[half, 7] == 64).all()
+    assert torch.equal(scale, (t[:, 0] / 127).float())
