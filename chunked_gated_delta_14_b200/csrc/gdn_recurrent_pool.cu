@@ -102,10 +102,15 @@ __device__ __forceinline__ bool sequence(const PoolParams &p, int s, int *slot, 
 //
 // they (and the squares of k and q, since both sums are linear in them) cross the
 // block in one exchange through shared memory.
-template <int R, bool BF16, bool VEC>
-__device__ __forceinline__ void step(const PoolParams &p, int slot, int64_t t, int h, int slice, int slices) {
-    __shared__ float4 sums[2][kGroups][32];
-    __shared__ float dots[3][kGroups];
+template <int QUADS>
+struct StepShared {                      // of a block of up to QUADS column quads
+    float4 sums[2][kGroups][QUADS];
+    float dots[3][kGroups];
+};
+template <int R, bool BF16, bool VEC, int QUADS>
+__device__ __forceinline__ void step(const PoolParams &p, int slot, int64_t t, int h, int slice, int slices, StepShared<QUADS> &shared) {
+    auto &sums = shared.sums;
+    auto &dots = shared.dots;
     const int pitch = p.dv / 4, quads = pitch / slices;      // float4 a row, and of this block
     const int group = threadIdx.x / quads, quad = threadIdx.x % quads;
     const int col = (slice * quads + quad) * 4;
@@ -182,7 +187,8 @@ __global__ void __launch_bounds__(256, 2) recurrent_step_kernel(const PoolParams
         if ((int)threadIdx.x < wide) store_o(p, ((int64_t)t * p.H + h) * p.dv + slice * wide + threadIdx.x, 0.f);
         return;
     }
-    step<R, BF16, VEC>(p, slot, t, h, slice, slices);
+    __shared__ StepShared<32> shared;
+    step<R, BF16, VEC>(p, slot, t, h, slice, slices, shared);
 }
 
 __device__ __forceinline__ float xor_add(float x, int mask) { return x + __shfl_xor_sync(~0u, x, mask); }
@@ -270,10 +276,12 @@ __global__ void __launch_bounds__(W * 32, R < 16 ? 1 : LONG ? 8 / W : 12 / W) re
     constexpr int kMine = kBring / W;                // tokens of those a warp brings
     constexpr int kPer = (kDk + 31) / 32, kPerV = kWide / 32;   // numbers of k, v a lane brings
     constexpr int kDot = kThreads / (4 * kBring);    // threads that share a dot product
-    constexpr int kDotRounds = (kDk / 4 + kDot - 1) / kDot;     // fours of numbers each takes (d_k 16: some take none)
-    static_assert(kDotRounds >= 1 && kDotRounds * kDot >= kDk / 4, "every product is a whole row's");
+    constexpr int kParts = kDk / 4 < 8 ? kDk / 4 : 8;           // sums that a dot product is made of, whoever forms them
+    constexpr int kDotParts = kParts < kDot ? 1 : kParts / kDot;
+    static_assert(kDk / 4 % kParts == 0 && (kParts % kDot == 0 || kParts < kDot), "every product is a whole row's");
     __shared__ __align__(16) float ks[3][kBring][kDk], qs[3][kBring][kDk], vs[3][kBring][kWide];
     __shared__ __align__(16) float alphas[3][kBring], betas[3][kBring], kk[2][kBring][kFour], kq[2][kBring][kFour];
+    __shared__ StepShared<W * 4> one;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slices = p.dv / kWide;
     const int slice = blockIdx.x % slices, h = blockIdx.x / slices % p.H;
     int s = blockIdx.x / slices / p.H;
@@ -286,10 +294,16 @@ __global__ void __launch_bounds__(W * 32, R < 16 ? 1 : LONG ? 8 / W : 12 / W) re
         return;
     }
     // A single token as in the kernel above, which has no tokens to bring (256 such sequences of 16
-    // heads, 37 of them idle: 80 us, the other way 105); the block has the shape of a step's.
-    if (!LONG && end - begin == 1) {
-        if (p.vec) step<R, BF16, true>(p, slot, begin, h, slice, slices);
-        else step<R, BF16, false>(p, slot, begin, h, slice, slices);
+    // heads, 37 of them idle: 80 us, the other way 105); the block has the shape of a step's, NQ
+    // times.  Here and in the order of the products' sums the variants agree, so that what a
+    // sequence gives does not depend on the batch that chose the variant.
+    if (end - begin == 1) {
+#pragma unroll 1
+        for (int z = 0; z < NQ; ++z) {
+            if (z) __syncthreads();
+            if (p.vec) step<R, BF16, true>(p, slot, begin, h, slice * NQ + z, slices * NQ, one);
+            else step<R, BF16, false>(p, slot, begin, h, slice * NQ + z, slices * NQ, one);
+        }
         return;
     }
     const int group = lane >> 2, quad = lane & 3, hk = h / (p.H / p.Hk);
@@ -365,16 +379,25 @@ __global__ void __launch_bounds__(W * 32, R < 16 ? 1 : LONG ? 8 / W : 12 / W) re
     auto dots = [&](int b, int to) {
         const float4 *x = reinterpret_cast<const float4 *>(dot < 6 ? ks[b][dot_i] : qs[b][dot_i]) + part;
         const float4 *y = reinterpret_cast<const float4 *>(ks[b][four + dot_j]) + part;
-        float sum = 0.f;
+        // kParts sums of every kParts-th four, joined by halves: the same order in every variant
+        float sum[kDotParts];
 #pragma unroll
-        for (int m = 0; m < kDotRounds; ++m) {
-            if (kDk / 4 % kDot && part + m * kDot >= kDk / 4) break;
-            const float4 u = x[m * kDot], v = y[m * kDot];
-            sum = fmaf(u.x, v.x, fmaf(u.y, v.y, fmaf(u.z, v.z, fmaf(u.w, v.w, sum))));
+        for (int i = 0; i < kDotParts; ++i) {
+            sum[i] = 0.f;
+            if (kParts < kDot && part >= kParts) break;
+#pragma unroll
+            for (int m = 0; m < kDk / 4 / kParts; ++m) {
+                const float4 u = x[m * kParts + i * kDot], v = y[m * kParts + i * kDot];
+                sum[i] = fmaf(u.x, v.x, fmaf(u.y, v.y, fmaf(u.z, v.z, fmaf(u.w, v.w, sum[i]))));
+            }
         }
 #pragma unroll
-        for (int m = 1; m < kDot; m *= 2) sum = xor_add(sum, m);
-        if (part == 0) (dot < 6 ? kk : kq)[to][dot_i][dot_j] = sum;
+        for (int w = kDotParts / 2; w; w /= 2)
+#pragma unroll
+            for (int i = 0; i < w; ++i) sum[i] += sum[i + w];
+#pragma unroll
+        for (int m = kDot / 2; m; m /= 2) sum[0] = xor_add(sum[0], m);
+        if (part == 0) (dot < 6 ? kk : kq)[to][dot_i][dot_j] = sum[0];
     };
     auto rows_at = [&](const float *x, F2 (&y)[R / 2]) {
 #pragma unroll

@@ -209,8 +209,9 @@ def recurrent_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, alpha: Opti
     ``qk_norm_eps`` (> 0): q and k are divided by sqrt(sum of squares + qk_norm_eps) first.
 
     slots and cu_seqlens are read on the device: an entry out of bounds touches nothing
-    and is reported by ``device_check``.  A slot may be named once in a call.  Prompts
-    of hundreds of tokens run quicker through ``chunk_fwd``.
+    and is reported by ``device_check``.  A slot may be named once in a call.  A sequence's
+    results do not depend on the others of the call, to the last bit.  Prompts of hundreds
+    of tokens run quicker through ``chunk_fwd``.
     """
     if stream is not None:
         return _other_stream(stream, q, (q, k, v, alpha, beta, state, slots, cu_seqlens, out), lambda: recurrent_fwd(

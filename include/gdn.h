@@ -412,6 +412,8 @@ GDN_API gdn_status gdn_chunk_fwd_static_scratch(const gdn_fwd_args *args, void *
  *   recorded for gdn_device_check; such an entry counts as slot -1, such a
  *   range as empty.
  * - With qk_norm, q_t and k_t are first divided by sqrt(sum of squares + qk_eps).
+ * - What a sequence gives, o and state, does not depend on the others of the call or
+ *   on its place among them, to the last bit.
  *
  * The state and all sums are fp32.  q, k, v may be parts of a wider row. */
 typedef struct {

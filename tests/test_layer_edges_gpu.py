@@ -165,3 +165,37 @@ def test_quantize_of_fp32_takes_the_nearest_step():
     half = y[:, 7] == 63.5                                        # not where column 7 was the largest itself
     assert half.sum() > 1900 and (q[half, 7] == 64).all()
     assert torch.equal(scale, (t[:, 0] / 127).float())
+
+
+@pytest.mark.parametrize("io", [BF, F])
+@pytest.mark.parametrize("dk,dv,Hk,H", [(128, 128, 2, 4), (16, 64, 1, 4), (32, 96, 2, 2), (64, 32, 1, 2), (16, 128, 4, 4)])
+def test_recurrent_gives_the_same_bits_whatever_is_beside_a_sequence(dk, dv, Hk, H, io):
+    """Alone, in a batch of short sequences, beside long ones, and in one of so many that its
+    blocks take whole heads; a single token without offsets too."""
+    mine = [1, 2, 3, 4, 5, 8, 13, 31, 1]
+    batches = [mine, mine + [2] * 40, mine + [300], [90, 0] + mine, mine + [40] * 90]
+    q, k, v, al, be, state, starts = make_rule(71, mine, Hk, H, dk, dv, io)
+    got = []
+    for lens in batches:
+        at = next(i for i in range(len(lens)) if lens[i:i + len(mine)] == mine)
+        Q, K, V, A, B, s, st = make_rule(72, lens, Hk, H, dk, dv, io)
+        a, e = st[at], st[at + len(mine)]
+        for x, y in ((Q, q), (K, k), (V, v), (A, al), (B, be)):
+            x[a:e] = y
+        s[at:at + len(mine)] = state
+        o = gdn.recurrent_fwd(Q, K, V, A, B, s, None, i32(st), qk_norm_eps=1e-6)
+        got.append((o[a:e].clone(), s[at:at + len(mine)].clone()))
+    for i, n in enumerate(mine):
+        a, e = starts[i], starts[i + 1]
+        s = state[i:i + 1].clone()
+        o = gdn.recurrent_fwd(q[a:e], k[a:e], v[a:e], al[a:e], be[a:e], s, None, i32([0, n]), qk_norm_eps=1e-6)
+        if n == 1:
+            s1 = state[i:i + 1].clone()
+            o1 = gdn.recurrent_fwd(q[a:e], k[a:e], v[a:e], al[a:e], be[a:e], s1, qk_norm_eps=1e-6)
+            assert torch.equal(o, o1) and torch.equal(s, s1)
+            P = 320 // H                                         # enough that a block takes more columns
+            s2 = state[i:i + 1].repeat(P, 1, 1, 1)
+            o2 = gdn.recurrent_fwd(*(x[a:e].repeat(P, *[1] * (x.dim() - 1)) for x in (q, k, v, al, be)), s2, qk_norm_eps=1e-6)
+            assert torch.equal(o2, o.repeat(P, 1, 1)) and torch.equal(s2, s.repeat(P, 1, 1, 1))
+        for j, (go, gs) in enumerate(got):
+            assert torch.equal(go[a:e], o) and torch.equal(gs[i], s[0]), (n, j)
