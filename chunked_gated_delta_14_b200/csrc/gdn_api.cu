@@ -328,20 +328,21 @@ int32_t gdn_select_segments(const gdn_fwd_args *args) {
 }
 
 gdn_status gdn_device_check(void *stream) {
+    // a kernel's word is read, and with that cleared, only when those before it were clean: of
+    // several that are set each call reports one
     cudaError_t e = cudaSuccess;
-    const unsigned int code = gdn::tc_read_and_clear_error(reinterpret_cast<cudaStream_t>(stream), &e);
-    if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "device check: %s", cudaGetErrorString(e));
-    const unsigned int fcode = gdn::fused_read_and_clear_error(&e);
+    unsigned int code = gdn::tc_read_and_clear_error(reinterpret_cast<cudaStream_t>(stream), &e);
     if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "device check: %s", cudaGetErrorString(e));
     if (code) return fail(GDN_ERR_DEVICE_CHECK, "split tensor-core kernel wait %u gave up", code);
-    const unsigned int pcode = gdn::pool_read_and_clear_error(&e);
+    code = gdn::fused_read_and_clear_error(&e);
     if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "device check: %s", cudaGetErrorString(e));
-    const unsigned int mcode = gdn::int8_matmul_read_and_clear_error(&e);
+    if (code) return fail(GDN_ERR_DEVICE_CHECK, "fused tensor-core kernel wait %u gave up", code);
+    code = gdn::pool_read_and_clear_error(&e);
     if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "device check: %s", cudaGetErrorString(e));
-    if (fcode) return fail(GDN_ERR_DEVICE_CHECK, "fused tensor-core kernel wait %u gave up", fcode);
-    if (pcode)
-        return fail(GDN_ERR_DEVICE_CHECK, "recurrent_fwd: slot or cu_seqlens of sequence %u out of bounds", pcode - 1);
-    if (mcode) return fail(GDN_ERR_DEVICE_CHECK, "int8 product kernel wait %u gave up", mcode);
+    if (code) return fail(GDN_ERR_DEVICE_CHECK, "recurrent_fwd: slot or cu_seqlens of sequence %u out of bounds", code - 1);
+    code = gdn::int8_matmul_read_and_clear_error(&e);
+    if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "device check: %s", cudaGetErrorString(e));
+    if (code) return fail(GDN_ERR_DEVICE_CHECK, "int8 product kernel wait %u gave up", code);
     g_msg[0] = 0;
     return GDN_OK;
 }
