@@ -281,4 +281,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_layer", "Quick way to the decode-
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__layer() { return PyModule_Create(&module); }
+// Nothing of torch is touched before layer.py has compared built_for with the torch that is there.
+PyMODINIT_FUNC PyInit__layer() {
+    PyObject *m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "built_for", GDN_BUILT_FOR) < 0) Py_CLEAR(m);
+    return m;
+}

@@ -17,6 +17,7 @@ from typing import Optional, Tuple
 
 import torch
 
+from .build import binding_for
 from .gdn import GDN_BF16, GDN_F32, GDN_OK, GDNError, last_error, lib
 
 ROWS_PLAIN, ROWS_NORM, ROWS_GATED = 0, 1, 2
@@ -67,7 +68,7 @@ _empty = torch.empty_strided          # a third quicker than torch.empty
 
 
 class _NoQuick:
-    """In place of the quick binding where it was not built: every call goes the long way."""
+    """In place of the quick binding where it was not built for this torch: every call goes the long way."""
     recurrent_fwd = add_rms_norm_int8 = gated_rms_norm_int8 = quantize_int8 = int8_matmul = staticmethod(lambda *a: None)
 
 
@@ -82,6 +83,8 @@ def _bind_quick():
     try:
         from . import _layer
     except ImportError:
+        _layer = None
+    if getattr(_layer, "built_for", None) != binding_for():      # torch's C++ tensors change between releases
         _quick = _NoQuick
     else:
         _layer.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (

@@ -3,8 +3,10 @@ import os
 import subprocess
 
 import pytest
+import torch
 
 import chunked_gated_delta_14_b200 as gdn
+import chunked_gated_delta_14_b200.layer as L
 from chunked_gated_delta_14_b200 import build as gbuild
 
 CSRC = os.path.join(os.path.dirname(os.path.abspath(gdn.__file__)), "csrc")
@@ -53,3 +55,42 @@ def test_device_check_reports_every_word(tmp_path):
                            "-Xlinker", "--unresolved-symbols=ignore-all"])
     out = subprocess.check_output([exe]).decode().split()
     assert out == [str(bin(i).count("1")) for i in range(16)]
+
+
+@pytest.fixture
+def binding_elsewhere(tmp_path, monkeypatch):
+    """build.py's binding in a folder of its own, made by a compiler that writes a line each time."""
+    cxx = tmp_path / "cxx"
+    cxx.write_text("#!/bin/sh\nwhile [ \"$1\" != -o ]; do shift; done\necho built > \"$2\"\necho run >> " + str(tmp_path / "runs") + "\n")
+    cxx.chmod(0o755)
+    monkeypatch.setenv("CXX", str(cxx))
+    monkeypatch.setattr(gbuild, "BINDING", str(tmp_path / "_layer.so"))
+    runs = tmp_path / "runs"
+    return lambda: len(runs.read_text().split()) if runs.exists() else 0
+
+
+def test_binding_is_rebuilt_for_another_torch(binding_elsewhere, monkeypatch):
+    assert not gbuild.binding_is_current()
+    for _ in range(2):
+        gbuild.build_binding()
+    assert binding_elsewhere() == 1 and gbuild.binding_is_current()
+    monkeypatch.setattr(torch, "__version__", "0.0.1+other")
+    assert not gbuild.binding_is_current()
+    gbuild.build_binding()
+    assert binding_elsewhere() == 2 and gbuild.binding_is_current()
+
+
+def test_binding_of_another_torch_is_not_used(monkeypatch):
+    monkeypatch.setattr(L, "_quick", None)
+    gbuild.build_binding()
+    from chunked_gated_delta_14_b200 import _layer
+    assert L._bind_quick() is _layer and _layer.built_for == gbuild.binding_for()
+    monkeypatch.setattr(torch, "__version__", "0.0.1+other")
+    assert L._bind_quick() is L._NoQuick
+
+
+@pytest.mark.parametrize("cxx", ["/bin/false", "/nowhere/cxx"])
+def test_library_builds_without_a_host_compiler_for_the_binding(binding_elsewhere, cxx, monkeypatch, capsys):
+    monkeypatch.setenv("CXX", cxx)
+    assert gbuild.build() == gbuild.LIB and os.path.exists(gbuild.LIB)
+    assert "not built" in capsys.readouterr().err and not gbuild.binding_is_current()
