@@ -71,6 +71,13 @@ int32_t size(Call &c, int64_t n) {
     return (int32_t)n;
 }
 
+// Python's lock is free while a call allocates and launches: both may wait (for memory, or for a
+// full queue), and other threads, host callbacks of the stream among them, go on meanwhile.
+struct Unlocked {
+    PyThreadState *state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 PyObject *wrap(const at::Tensor &t) { return THPVariable_Wrap(t); }
 PyObject *none() { Py_RETURN_NONE; }
 
@@ -97,12 +104,6 @@ PyObject *recurrent_fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     g.rows = size(c, N); g.seqs = size(c, S); g.H = size(c, H); g.Hk = size(c, q->size(1));
     g.dk = size(c, q->size(2)); g.dv = size(c, v->size(2)); g.pool = size(c, state->size(0));
     if (!c.fits) return none();
-    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)c.device);
-    at::Tensor made;
-    if (!out) {
-        made = cu ? at::zeros(v->sizes(), c.options(od)) : at::empty(v->sizes(), c.options(od));
-        out = &made;
-    }
     g.io_dtype = code(io); g.o_dtype = code(od);
     g.qk_norm = a[8] != Py_None;
     g.qk_eps = g.qk_norm ? (float)PyFloat_AS_DOUBLE(a[8]) : 0.f;
@@ -110,23 +111,35 @@ PyObject *recurrent_fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     g.q_row = q->stride(0); g.q_head = q->stride(1); g.k_row = k->stride(0); g.k_head = k->stride(1);
     g.v_row = v->stride(0); g.v_head = v->stride(1);
     g.alpha = ptr<float>(alpha); g.beta = ptr<float>(beta); g.alpha_row = row(alpha); g.beta_row = row(beta);
-    g.cu_seqlens = ptr<int32_t>(cu); g.slots = ptr<int32_t>(slots); g.state = ptr<float>(state); g.o = ptr(out);
-    const gdn_status s = recurrent_fn(&g, c.stream());
+    g.cu_seqlens = ptr<int32_t>(cu); g.slots = ptr<int32_t>(slots); g.state = ptr<float>(state);
+    at::Tensor made;
+    gdn_status s;
+    {
+        const Unlocked unlocked;
+        const c10::cuda::CUDAGuard guard((c10::DeviceIndex)c.device);
+        if (!out) {
+            made = cu ? at::zeros(v->sizes(), c.options(od)) : at::empty(v->sizes(), c.options(od));
+            out = &made;
+        }
+        g.o = ptr(out);
+        s = recurrent_fn(&g, c.stream());
+    }
     if (s != GDN_OK) return PyLong_FromLong(s);
     if (!made.defined()) { Py_INCREF(a[10]); return a[10]; }
     return wrap(made);
     END_HANDLE_TH_ERRORS
 }
 
-// Rows of steps that start on 16 bytes, and their scales, into g.
+// Rows of steps that start on 16 bytes, and their scales, and the call that fills them.
 struct Steps {
     at::Tensor q, scale;
-    Steps(const Call &c, int64_t rows, int64_t width, gdn_rows_args &g) {
+    gdn_status make(const Call &c, int64_t rows, int64_t width, gdn_rows_args &g) {
         const int64_t pitch = (width + 15) / 16 * 16;
         q = at::empty_strided({rows, width}, {pitch, 1}, c.options(at::kChar));
         scale = at::empty({rows}, c.options(at::kFloat));
         g.rows = (int32_t)rows; g.width = (int32_t)width;
         g.q = ptr<int8_t>(&q); g.q_row = pitch; g.scale = ptr<float>(&scale);
+        return rows_fn(&g, c.stream());
     }
 };
 PyObject *pair_of(const Steps &y) {
@@ -145,11 +158,15 @@ PyObject *quantize_int8(PyObject *, PyObject *const *a, Py_ssize_t n) {
     c.need(is_io(x->scalar_type()));
     size(c, x->size(0)); size(c, x->size(1));
     if (!c.fits) return none();
-    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)c.device);
     gdn_rows_args g{};
-    const Steps y(c, x->size(0), x->size(1), g);
     g.op = GDN_ROWS_PLAIN; g.x_dtype = code(x->scalar_type()); g.x = ptr(x); g.x_row = row(x);
-    const gdn_status s = rows_fn(&g, c.stream());
+    Steps y;
+    gdn_status s;
+    {
+        const Unlocked unlocked;
+        const c10::cuda::CUDAGuard guard((c10::DeviceIndex)c.device);
+        s = y.make(c, x->size(0), x->size(1), g);
+    }
     return s == GDN_OK ? pair_of(y) : PyLong_FromLong(s);
     END_HANDLE_TH_ERRORS
 }
@@ -167,19 +184,21 @@ PyObject *add_rms_norm_int8(PyObject *, PyObject *const *a, Py_ssize_t n) {
     c.need(!out || (out->scalar_type() == r->scalar_type() && out->sizes() == x->sizes()));
     size(c, x->size(0)); size(c, x->size(1));
     if (!c.fits) return none();
-    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)c.device);
     gdn_rows_args g{};
-    const Steps y(c, x->size(0), x->size(1), g);
-    at::Tensor made;
-    if (r && !out) { made = at::empty(x->sizes(), c.options(r->scalar_type())); out = &made; }
     g.op = GDN_ROWS_NORM; g.eps = (float)PyFloat_AS_DOUBLE(a[3]);
     g.x_dtype = code(x->scalar_type()); g.x = ptr(x); g.x_row = row(x);
     if (w) { g.weight_dtype = code(w->scalar_type()); g.weight = ptr(w); }
-    if (r) {
-        g.residual_dtype = code(r->scalar_type()); g.residual = ptr(r); g.residual_row = row(r);
-        g.residual_out = ptr(out); g.residual_out_row = row(out);
+    if (r) { g.residual_dtype = code(r->scalar_type()); g.residual = ptr(r); g.residual_row = row(r); }
+    Steps y;
+    at::Tensor made;
+    gdn_status s;
+    {
+        const Unlocked unlocked;
+        const c10::cuda::CUDAGuard guard((c10::DeviceIndex)c.device);
+        if (r && !out) { made = at::empty(x->sizes(), c.options(r->scalar_type())); out = &made; }
+        if (out) { g.residual_out = ptr(out); g.residual_out_row = row(out); }
+        s = y.make(c, x->size(0), x->size(1), g);
     }
-    const gdn_status s = rows_fn(&g, c.stream());
     if (s != GDN_OK) return PyLong_FromLong(s);
     PyObject *t = PyTuple_New(3);
     if (!t) return nullptr;
@@ -205,14 +224,18 @@ PyObject *gated_rms_norm_int8(PyObject *, PyObject *const *a, Py_ssize_t n) {
     c.need((x->stride(1) == d && gate->stride(1) == d) || H == 1);
     size(c, x->size(0)); size(c, H * d); size(c, d);
     if (!c.fits) return none();
-    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)c.device);
     gdn_rows_args g{};
-    const Steps y(c, x->size(0), H * d, g);
     g.op = GDN_ROWS_GATED; g.head = (int32_t)d; g.eps = (float)PyFloat_AS_DOUBLE(a[3]);
     g.x_dtype = code(x->scalar_type()); g.x = ptr(x); g.x_row = row(x);
     g.gate = ptr(gate); g.gate_row = row(gate);
     if (w) { g.weight_dtype = code(w->scalar_type()); g.weight = ptr(w); }
-    const gdn_status s = rows_fn(&g, c.stream());
+    Steps y;
+    gdn_status s;
+    {
+        const Unlocked unlocked;
+        const c10::cuda::CUDAGuard guard((c10::DeviceIndex)c.device);
+        s = y.make(c, x->size(0), H * d, g);
+    }
     return s == GDN_OK ? pair_of(y) : PyLong_FromLong(s);
     END_HANDLE_TH_ERRORS
 }
@@ -234,18 +257,23 @@ PyObject *int8_matmul(PyObject *, PyObject *const *a, Py_ssize_t n) {
     gdn_int8_matmul_args g{};
     g.M = size(c, M); g.N = size(c, N); g.K = size(c, K);
     if (!c.fits) return none();
-    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)c.device);
-    at::Tensor made, workspace;
-    if (!out) { made = at::empty({M, N}, c.options(od)); out = &made; }
     g.out_dtype = code(od);
-    g.x = ptr<int8_t>(x); g.w = ptr<int8_t>(w); g.x_row = row(x); g.w_row = row(w); g.out_row = made.defined() ? N : row(out);
-    g.x_scale = ptr<float>(xs); g.w_scale = ptr<float>(ws); g.bias = ptr<float>(bias); g.out = ptr(out);
-    g.workspace_bytes = matmul_workspace_fn(&g);
-    if (g.workspace_bytes) {     // not kept: a call's copies belong to its stream, or its graph
-        workspace = at::empty({(int64_t)g.workspace_bytes}, c.options(at::kByte));
-        g.workspace = workspace.data_ptr();
+    g.x = ptr<int8_t>(x); g.w = ptr<int8_t>(w); g.x_row = row(x); g.w_row = row(w);
+    g.x_scale = ptr<float>(xs); g.w_scale = ptr<float>(ws); g.bias = ptr<float>(bias);
+    at::Tensor made, workspace;
+    gdn_status s;
+    {
+        const Unlocked unlocked;
+        const c10::cuda::CUDAGuard guard((c10::DeviceIndex)c.device);
+        if (!out) { made = at::empty({M, N}, c.options(od)); out = &made; }
+        g.out = ptr(out); g.out_row = made.defined() ? N : row(out);
+        g.workspace_bytes = matmul_workspace_fn(&g);
+        if (g.workspace_bytes) {     // not kept: a call's copies belong to its stream, or its graph
+            workspace = at::empty({(int64_t)g.workspace_bytes}, c.options(at::kByte));
+            g.workspace = workspace.data_ptr();
+        }
+        s = matmul_fn(&g, c.stream());
     }
-    const gdn_status s = matmul_fn(&g, c.stream());
     if (s != GDN_OK) return PyLong_FromLong(s);
     if (!made.defined()) { Py_INCREF(a[6]); return a[6]; }
     return wrap(made);

@@ -199,3 +199,44 @@ def test_recurrent_gives_the_same_bits_whatever_is_beside_a_sequence(dk, dv, Hk,
             assert torch.equal(o2, o.repeat(P, 1, 1)) and torch.equal(s2, s.repeat(P, 1, 1, 1))
         for j, (go, gs) in enumerate(got):
             assert torch.equal(go[a:e], o) and torch.equal(gs[i], s[0]), (n, j)
+
+
+def test_other_threads_run_while_a_call_waits(tmp_path):
+    """The quick binding over functions that wait 0.3 s, as a launch into a full queue does: Python's
+    lock is free meanwhile."""
+    import ctypes
+    import subprocess
+    import threading
+    import time
+    from chunked_gated_delta_14_b200 import _layer
+    (tmp_path / "wait.c").write_text("#include <unistd.h>\nint waits(const void *a, void *s) { usleep(300000); return 1; }\n"
+                                     "unsigned long long none(const void *a) { return 0; }\n")
+    subprocess.check_call(["gcc", "-shared", "-fPIC", str(tmp_path / "wait.c"), "-o", str(tmp_path / "wait.so")])
+    so = ctypes.CDLL(str(tmp_path / "wait.so"))
+    at = lambda f: ctypes.cast(f, ctypes.c_void_p).value  # noqa: E731
+    x, i8, s = torch.ones(4, 64, device="cuda"), torch.ones(4, 64, device="cuda", dtype=torch.int8), torch.ones(4, device="cuda")
+    q, state = x.view(4, 1, 64), torch.zeros(4, 1, 64, 64, device="cuda")
+    calls = [lambda: _layer.quantize_int8(x), lambda: _layer.add_rms_norm_int8(x, None, x, 1e-6, None),
+             lambda: _layer.gated_rms_norm_int8(x.view(4, 2, 32), x.view(4, 2, 32), None, 1e-6),
+             lambda: _layer.int8_matmul(i8, s, i8, s, None, F, None),
+             lambda: _layer.recurrent_fwd(q, q, q, None, None, state, None, None, None, None, None)]
+    turns, done = [0], threading.Event()
+
+    def turn():
+        while not done.is_set():
+            turns[0] += 1
+            time.sleep(0.002)
+    thread = threading.Thread(target=turn)
+    thread.start()
+    try:
+        _layer.bind(at(so.waits), at(so.waits), at(so.waits), at(so.none), gdn.abi_version())
+        for call in calls:
+            before = turns[0]
+            assert call() == 1
+            assert turns[0] - before > 20
+    finally:
+        done.set()
+        thread.join()
+        gdn.layer._bind_quick()
+    assert type(_layer.quantize_int8(x)) is tuple
+    gdn.device_check()
