@@ -1,6 +1,6 @@
 // Quick way from Python to the decode-layer operators: what layer.py does for a call of
-// the usual form (plain tensors of the usual dimensions on one device), without a Python
-// call for every shape, stride and pointer, which cost a small call more than its launch.
+// the usual form (plain tensors on one device, with rows), without a Python call for every
+// shape, stride and pointer, which cost a small call more than its launch.
 // Each function returns
 //   None              the call is not of that form: layer.py checks it and says what is wrong,
 //                     or makes the call itself;
@@ -31,18 +31,23 @@ struct Call {
     bool grad = c10::GradMode::is_enabled();
     bool fits = true;
 
-    // A plain tensor with `dims` dimensions, contiguous in the last, on the call's device.
-    const at::Tensor *tensor(PyObject *o, int64_t dims) {
+    // A plain tensor on the call's device, with `least` dimensions or more, contiguous in the last.
+    const at::Tensor *any(PyObject *o, int64_t least) {
         if (!fits || !THPVariable_CheckExact(o)) { fits = false; return nullptr; }
         const at::Tensor &t = THPVariable_Unpack(o);
-        if (!t.is_cuda() || t.layout() != at::kStrided || t.dim() != dims || t.stride(dims - 1) != 1 ||
-            (grad && t.requires_grad())) {
+        if (!t.is_cuda() || t.layout() != at::kStrided || t.dim() < least || (t.dim() && t.stride(-1) != 1) || (grad && t.requires_grad())) {
             fits = false;
             return nullptr;
         }
         if (device < 0) device = t.device().index();
         fits = device == t.device().index();
         return fits ? &t : nullptr;
+    }
+    // With `dims` dimensions.
+    const at::Tensor *tensor(PyObject *o, int64_t dims) {
+        const at::Tensor *t = any(o, dims);
+        if (t && t->dim() != dims) { fits = false; t = nullptr; }
+        return t;
     }
     const at::Tensor *tensor(PyObject *o, int64_t dims, at::ScalarType type) {
         const at::Tensor *t = tensor(o, dims);
@@ -64,6 +69,39 @@ int32_t code(at::ScalarType t) { return t == at::kBFloat16 ? GDN_BF16 : GDN_F32;
 template <typename T = void>
 T *ptr(const at::Tensor *t) { return t ? static_cast<T *>(t->data_ptr()) : nullptr; }
 int64_t row(const at::Tensor *t) { return t ? t->stride(0) : 0; }
+
+// A tensor seen as rows of its last `last` dimensions: their number, and their stride where they
+// are one run, else the call is left to layer.py (as one of no rows is).
+struct Rows {
+    int64_t rows = 1, stride = 0;
+    Rows(Call &c, const at::Tensor *t, int64_t last) {
+        if (!t) return;
+        int64_t next = -1;               // the stride that goes on with the run
+        for (int64_t d = t->dim() - last - 1; d >= 0; --d) {
+            const int64_t n = t->size(d);
+            if (n == 1) continue;
+            c.need(n > 0 && (next < 0 || t->stride(d) == next));
+            if (next < 0) stride = t->stride(d);
+            next = t->stride(d) * n;
+            rows *= n;
+        }
+        c.need(rows <= INT32_MAX);
+    }
+};
+at::IntArrayRef lead(const at::Tensor *t, int64_t last) { return t->sizes().slice(0, t->dim() - last); }
+at::DimVector shape(at::IntArrayRef lead, int64_t width) {
+    at::DimVector s(lead.begin(), lead.end());
+    s.push_back(width);
+    return s;
+}
+// A Python number (eps), else the call is left to layer.py.
+double number(Call &c, PyObject *o) {
+    c.need(PyFloat_CheckExact(o) || PyLong_CheckExact(o));
+    if (!c.fits) return 0;
+    const double x = PyFloat_AsDouble(o);
+    if (PyErr_Occurred()) { PyErr_Clear(); c.fits = false; }     // a whole number past the range
+    return x;
+}
 
 // A size that the structs hold, else the call is left to layer.py.
 int32_t size(Call &c, int64_t n) {
@@ -90,7 +128,8 @@ PyObject *recurrent_fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const at::Tensor *alpha = c.maybe(a[3], 2, at::kFloat), *beta = c.maybe(a[4], 2, at::kFloat);
     const at::Tensor *slots = c.maybe(a[6], 1, at::kInt), *cu = c.maybe(a[7], 1, at::kInt);
     const at::Tensor *out = a[10] == Py_None ? nullptr : c.tensor(a[10], 3);
-    if (!c.fits || !(a[8] == Py_None || PyFloat_CheckExact(a[8]))) return none();
+    const double eps = a[8] == Py_None ? 0 : number(c, a[8]);
+    if (!c.fits) return none();
     const at::ScalarType io = q->scalar_type();
     const at::ScalarType od = a[9] != Py_None ? reinterpret_cast<THPDtype *>(a[9])->scalar_type : out ? out->scalar_type() : io;
     const int64_t N = q->size(0), H = v->size(1), S = cu ? cu->size(0) - 1 : N;
@@ -106,7 +145,7 @@ PyObject *recurrent_fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (!c.fits) return none();
     g.io_dtype = code(io); g.o_dtype = code(od);
     g.qk_norm = a[8] != Py_None;
-    g.qk_eps = g.qk_norm ? (float)PyFloat_AS_DOUBLE(a[8]) : 0.f;
+    g.qk_eps = (float)eps;
     g.q = ptr(q); g.k = ptr(k); g.v = ptr(v);
     g.q_row = q->stride(0); g.q_head = q->stride(1); g.k_row = k->stride(0); g.k_head = k->stride(1);
     g.v_row = v->stride(0); g.v_head = v->stride(1);
@@ -133,10 +172,13 @@ PyObject *recurrent_fwd(PyObject *, PyObject *const *a, Py_ssize_t n) {
 // Rows of steps that start on 16 bytes, and their scales, and the call that fills them.
 struct Steps {
     at::Tensor q, scale;
-    gdn_status make(const Call &c, int64_t rows, int64_t width, gdn_rows_args &g) {
+    gdn_status make(const Call &c, at::IntArrayRef lead, int64_t rows, int64_t width, gdn_rows_args &g) {
         const int64_t pitch = (width + 15) / 16 * 16;
-        q = at::empty_strided({rows, width}, {pitch, 1}, c.options(at::kChar));
-        scale = at::empty({rows}, c.options(at::kFloat));
+        at::DimVector strides = shape(lead, 1);
+        int64_t next = pitch;
+        for (int64_t d = (int64_t)lead.size() - 1; d >= 0; --d) { strides[d] = next; next *= lead[d]; }
+        q = at::empty_strided(shape(lead, width), strides, c.options(at::kChar));
+        scale = at::empty(lead, c.options(at::kFloat));
         g.rows = (int32_t)rows; g.width = (int32_t)width;
         g.q = ptr<int8_t>(&q); g.q_row = pitch; g.scale = ptr<float>(&scale);
         return rows_fn(&g, c.stream());
@@ -153,19 +195,20 @@ PyObject *quantize_int8(PyObject *, PyObject *const *a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     if (n != 1) return none();
     Call c;
-    const at::Tensor *x = c.tensor(a[0], 2);
+    const at::Tensor *x = c.any(a[0], 1);
+    const Rows xr(c, x, 1);
     if (!c.fits) return none();
     c.need(is_io(x->scalar_type()));
-    size(c, x->size(0)); size(c, x->size(1));
+    size(c, x->size(-1));
     if (!c.fits) return none();
     gdn_rows_args g{};
-    g.op = GDN_ROWS_PLAIN; g.x_dtype = code(x->scalar_type()); g.x = ptr(x); g.x_row = row(x);
+    g.op = GDN_ROWS_PLAIN; g.x_dtype = code(x->scalar_type()); g.x = ptr(x); g.x_row = xr.stride;
     Steps y;
     gdn_status s;
     {
         const Unlocked unlocked;
         const c10::cuda::CUDAGuard guard((c10::DeviceIndex)c.device);
-        s = y.make(c, x->size(0), x->size(1), g);
+        s = y.make(c, lead(x, 1), xr.rows, x->size(-1), g);
     }
     return s == GDN_OK ? pair_of(y) : PyLong_FromLong(s);
     END_HANDLE_TH_ERRORS
@@ -174,21 +217,24 @@ PyObject *quantize_int8(PyObject *, PyObject *const *a, Py_ssize_t n) {
 // (x, weight, residual, eps, residual_out)
 PyObject *add_rms_norm_int8(PyObject *, PyObject *const *a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    if (n != 5 || !PyFloat_CheckExact(a[3]) || (a[2] == Py_None && a[4] != Py_None)) return none();
+    if (n != 5 || (a[2] == Py_None && a[4] != Py_None)) return none();
     Call c;
-    const at::Tensor *x = c.tensor(a[0], 2), *w = a[1] == Py_None ? nullptr : c.tensor(a[1], 1);
-    const at::Tensor *r = a[2] == Py_None ? nullptr : c.tensor(a[2], 2), *out = a[4] == Py_None ? nullptr : c.tensor(a[4], 2);
+    const at::Tensor *x = c.any(a[0], 1), *w = a[1] == Py_None ? nullptr : c.tensor(a[1], 1);
+    const at::Tensor *r = a[2] == Py_None ? nullptr : c.any(a[2], 1), *out = a[4] == Py_None ? nullptr : c.any(a[4], 1);
+    const Rows xr(c, x, 1), rr(c, r, 1), outr(c, out, 1);
+    const double eps = number(c, a[3]);
     if (!c.fits) return none();
-    c.need(is_io(x->scalar_type()) && (!w || (is_io(w->scalar_type()) && w->size(0) == x->size(1))));
+    const int64_t width = x->size(-1);
+    c.need(is_io(x->scalar_type()) && (!w || (is_io(w->scalar_type()) && w->size(0) == width)));
     c.need(!r || (is_io(r->scalar_type()) && r->sizes() == x->sizes()));
     c.need(!out || (out->scalar_type() == r->scalar_type() && out->sizes() == x->sizes()));
-    size(c, x->size(0)); size(c, x->size(1));
+    size(c, width);
     if (!c.fits) return none();
     gdn_rows_args g{};
-    g.op = GDN_ROWS_NORM; g.eps = (float)PyFloat_AS_DOUBLE(a[3]);
-    g.x_dtype = code(x->scalar_type()); g.x = ptr(x); g.x_row = row(x);
+    g.op = GDN_ROWS_NORM; g.eps = (float)eps;
+    g.x_dtype = code(x->scalar_type()); g.x = ptr(x); g.x_row = xr.stride;
     if (w) { g.weight_dtype = code(w->scalar_type()); g.weight = ptr(w); }
-    if (r) { g.residual_dtype = code(r->scalar_type()); g.residual = ptr(r); g.residual_row = row(r); }
+    if (r) { g.residual_dtype = code(r->scalar_type()); g.residual = ptr(r); g.residual_row = rr.stride; }
     Steps y;
     at::Tensor made;
     gdn_status s;
@@ -196,8 +242,8 @@ PyObject *add_rms_norm_int8(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const Unlocked unlocked;
         const c10::cuda::CUDAGuard guard((c10::DeviceIndex)c.device);
         if (r && !out) { made = at::empty(x->sizes(), c.options(r->scalar_type())); out = &made; }
-        if (out) { g.residual_out = ptr(out); g.residual_out_row = row(out); }
-        s = y.make(c, x->size(0), x->size(1), g);
+        if (out) { g.residual_out = ptr(out); g.residual_out_row = made.defined() ? width : outr.stride; }
+        s = y.make(c, lead(x, 1), xr.rows, width, g);
     }
     if (s != GDN_OK) return PyLong_FromLong(s);
     PyObject *t = PyTuple_New(3);
@@ -214,27 +260,29 @@ PyObject *add_rms_norm_int8(PyObject *, PyObject *const *a, Py_ssize_t n) {
 // (x, gate, weight, eps)
 PyObject *gated_rms_norm_int8(PyObject *, PyObject *const *a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    if (n != 4 || !PyFloat_CheckExact(a[3])) return none();
+    if (n != 4) return none();
     Call c;
-    const at::Tensor *x = c.tensor(a[0], 3), *gate = c.tensor(a[1], 3), *w = a[2] == Py_None ? nullptr : c.tensor(a[2], 1);
+    const at::Tensor *x = c.any(a[0], 2), *gate = c.any(a[1], 2), *w = a[2] == Py_None ? nullptr : c.tensor(a[2], 1);
+    const Rows xr(c, x, 2), gr(c, gate, 2);
+    const double eps = number(c, a[3]);
     if (!c.fits) return none();
-    const int64_t H = x->size(1), d = x->size(2);
+    const int64_t H = x->size(-2), d = x->size(-1);
     c.need(is_io(x->scalar_type()) && gate->scalar_type() == x->scalar_type() && gate->sizes() == x->sizes());
     c.need(!w || (is_io(w->scalar_type()) && w->size(0) == d));
-    c.need((x->stride(1) == d && gate->stride(1) == d) || H == 1);
-    size(c, x->size(0)); size(c, H * d); size(c, d);
+    c.need((x->stride(-2) == d && gate->stride(-2) == d) || H == 1);
+    size(c, H * d); size(c, d);
     if (!c.fits) return none();
     gdn_rows_args g{};
-    g.op = GDN_ROWS_GATED; g.head = (int32_t)d; g.eps = (float)PyFloat_AS_DOUBLE(a[3]);
-    g.x_dtype = code(x->scalar_type()); g.x = ptr(x); g.x_row = row(x);
-    g.gate = ptr(gate); g.gate_row = row(gate);
+    g.op = GDN_ROWS_GATED; g.head = (int32_t)d; g.eps = (float)eps;
+    g.x_dtype = code(x->scalar_type()); g.x = ptr(x); g.x_row = xr.stride;
+    g.gate = ptr(gate); g.gate_row = gr.stride;
     if (w) { g.weight_dtype = code(w->scalar_type()); g.weight = ptr(w); }
     Steps y;
     gdn_status s;
     {
         const Unlocked unlocked;
         const c10::cuda::CUDAGuard guard((c10::DeviceIndex)c.device);
-        s = y.make(c, x->size(0), H * d, g);
+        s = y.make(c, lead(x, 2), xr.rows, H * d, g);
     }
     return s == GDN_OK ? pair_of(y) : PyLong_FromLong(s);
     END_HANDLE_TH_ERRORS
@@ -245,28 +293,28 @@ PyObject *int8_matmul(PyObject *, PyObject *const *a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
     if (n != 7 || !THPDtype_Check(a[5])) return none();
     Call c;
-    const at::Tensor *x = c.tensor(a[0], 2, at::kChar), *xs = c.tensor(a[1], 1, at::kFloat);
-    const at::Tensor *w = c.tensor(a[2], 2, at::kChar), *ws = c.tensor(a[3], 1, at::kFloat);
-    const at::Tensor *bias = c.maybe(a[4], 1, at::kFloat);
+    const at::Tensor *x = c.any(a[0], 1), *xs = c.any(a[1], 0), *w = c.tensor(a[2], 2, at::kChar), *ws = c.tensor(a[3], 1, at::kFloat);
+    const at::Tensor *bias = c.maybe(a[4], 1, at::kFloat), *out = a[6] == Py_None ? nullptr : c.any(a[6], 1);
     const at::ScalarType od = reinterpret_cast<THPDtype *>(a[5])->scalar_type;
-    const at::Tensor *out = c.maybe(a[6], 2, od);
+    const Rows xr(c, x, 1), outr(c, out, 1);
     if (!c.fits) return none();
-    const int64_t M = x->size(0), K = x->size(1), N = w->size(0);
-    c.need(is_io(od) && w->size(1) == K && xs->size(0) == M && ws->size(0) == N && (!bias || bias->size(0) == N));
-    c.need(!out || (out->size(0) == M && out->size(1) == N));
+    const int64_t K = x->size(-1), N = w->size(0);
+    c.need(x->scalar_type() == at::kChar && xs->scalar_type() == at::kFloat && xs->sizes() == lead(x, 1) && xs->is_contiguous());
+    c.need(is_io(od) && w->size(1) == K && ws->size(0) == N && (!bias || bias->size(0) == N));
+    c.need(!out || (out->scalar_type() == od && out->size(-1) == N && lead(out, 1) == lead(x, 1)));
     gdn_int8_matmul_args g{};
-    g.M = size(c, M); g.N = size(c, N); g.K = size(c, K);
+    g.M = (int32_t)xr.rows; g.N = size(c, N); g.K = size(c, K);
     if (!c.fits) return none();
     g.out_dtype = code(od);
-    g.x = ptr<int8_t>(x); g.w = ptr<int8_t>(w); g.x_row = row(x); g.w_row = row(w);
+    g.x = ptr<int8_t>(x); g.w = ptr<int8_t>(w); g.x_row = xr.stride; g.w_row = row(w);
     g.x_scale = ptr<float>(xs); g.w_scale = ptr<float>(ws); g.bias = ptr<float>(bias);
     at::Tensor made, workspace;
     gdn_status s;
     {
         const Unlocked unlocked;
         const c10::cuda::CUDAGuard guard((c10::DeviceIndex)c.device);
-        if (!out) { made = at::empty({M, N}, c.options(od)); out = &made; }
-        g.out = ptr(out); g.out_row = made.defined() ? N : row(out);
+        if (!out) { made = at::empty(shape(lead(x, 1), N), c.options(od)); out = &made; }
+        g.out = ptr(out); g.out_row = made.defined() ? N : outr.stride;
         g.workspace_bytes = matmul_workspace_fn(&g);
         if (g.workspace_bytes) {     // not kept: a call's copies belong to its stream, or its graph
             workspace = at::empty({(int64_t)g.workspace_bytes}, c.options(at::kByte));

@@ -50,8 +50,7 @@ class Int8MatmulArgs(ctypes.Structure):
 
 
 def _packer(mirror):
-    """``pack(*fields)`` -> the struct's bytes: several times quicker than filling a ctypes
-    struct field by field."""
+    """``pack(*fields)`` -> the struct's bytes, from fields in order."""
     codes = {_I: "i", _F: "f", _P: "P", _Q: "q", _U: "Q"}
     s = struct.Struct("@" + "".join(codes[t] for _, t in mirror._fields_))
     assert s.size == ctypes.sizeof(mirror), mirror
@@ -60,11 +59,6 @@ def _packer(mirror):
 
 _pack_recurrent, _pack_rows, _pack_matmul = (_packer(m) for m in (RecurrentArgs, RowsArgs, Int8MatmulArgs))
 _DTYPES = {torch.float32: GDN_F32, torch.bfloat16: GDN_BF16}
-_functions = {}
-# torch.cuda.current_stream(i).cuda_stream and current_device(), without their objects (2 us a call)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
-_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-_empty = torch.empty_strided          # a third quicker than torch.empty
 
 
 class _NoQuick:
@@ -97,6 +91,10 @@ def _failed(status):
     raise GDNError(status, last_error())
 
 
+_IO = (torch.bfloat16, torch.float32)
+_F32, _I32, _I8 = (torch.float32,), (torch.int32,), (torch.int8,)
+
+
 def _check(t, name, shape, dtypes, device):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -110,12 +108,13 @@ def _check(t, name, shape, dtypes, device):
         raise ValueError(f"{name} requires a gradient: the decode-layer operators have none")
     if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
+    if any(n > 2 ** 31 - 1 for n in t.shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}: sizes up to 2^31 - 1 are taken")
 
 
 def _first(t, name, dims, dtypes):
     """Checks the tensor whose shape and device the others follow."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
+    _tensors(**{name: t})
     if t.device.type != "cuda":
         raise ValueError(f"{name} must be a CUDA tensor (got {t.device})")
     if t.dim() < dims:
@@ -123,18 +122,31 @@ def _first(t, name, dims, dtypes):
     _check(t, name, t.shape, dtypes, t.device)
 
 
-_IO = (torch.bfloat16, torch.float32)
-_F32, _I32, _I8 = (torch.float32,), (torch.int32,), (torch.int8,)
+def _tensors(**named):
+    for name in named:
+        if not isinstance(named[name], torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+
+
+def _code(dt):
+    if dt not in _DTYPES:
+        raise TypeError(f"unsupported dtype {dt}; use torch.bfloat16 or torch.float32")
+    return _DTYPES[dt]
+
+
+def _ptr(t):
+    return 0 if t is None else t.data_ptr()
 
 
 def _rows(t, name):
     """(rows, stride) of t seen as rows of its last dimension."""
-    if t.dim() == 2:
-        return t.shape[0], t.stride()[0]
-    try:
-        t = t.view(-1, t.shape[-1])
-    except RuntimeError:
-        raise ValueError(f"{name}: the leading dimensions must be one run of rows with one stride") from None
+    if t.dim() != 2:
+        try:
+            t = t.view(-1, t.shape[-1])
+        except RuntimeError:
+            raise ValueError(f"{name}: the leading dimensions must be one run of rows with one stride") from None
+    if t.shape[0] > 2 ** 31 - 1:
+        raise ValueError(f"{name} has {t.shape[0]} rows: up to 2^31 - 1 are taken")
     return t.shape[0], t.stride(0)
 
 
@@ -155,12 +167,8 @@ def _other_stream(stream, first, tensors, call):
 
 def _launch(name, packed, i):
     """Raw call on device i's current stream; raises GDNError on a non-OK status."""
-    fn = _functions.get(name) or _functions.setdefault(name, getattr(lib(), name))
-    if _current_device() == i:
-        s = fn(packed, _raw_stream(i))
-    else:
-        with torch.cuda.device(i):
-            s = fn(packed, _raw_stream(i))
+    with torch.cuda.device(i):
+        s = getattr(lib(), name)(packed, torch.cuda.current_stream(i).cuda_stream)
     if s != GDN_OK:
         raise GDNError(s, last_error())
 
@@ -222,71 +230,19 @@ def recurrent_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, alpha: Opti
     r = (_quick or _bind_quick()).recurrent_fwd(q, k, v, alpha, beta, state, slots, cu_seqlens, qk_norm_eps, o_dtype, out)
     if r is not None:
         return r if type(r) is not int else _failed(r)
-    # What a correct call looks like, tested in place; _recurrent_refuse says what is wrong with another.
-    try:
-        N, Hk, dk = shape = q.shape
-        _, H, dv = v.shape
-        io, i, S = q.dtype, q.get_device(), N
-        P, gates = state.shape[0], (N, H)
-        qr, qh, q1 = q.stride()
-        kr, kh, k1 = k.stride()
-        vr, vh, v1 = v.stride()
-        ap = bp = ar = br = cp = sp = 0
-        fits = (i >= 0 and k.shape == shape and v.shape == (N, H, dv) and k.dtype is io and v.dtype is io and q1 == k1 == v1 == 1
-                and k.get_device() == i and v.get_device() == i and state.dtype is torch.float32 and state.get_device() == i
-                and state.shape == (P, H, dk, dv) and state.is_contiguous())
-        if alpha is not None:
-            ar, a1 = alpha.stride()
-            ap = alpha.data_ptr()
-            fits = fits and a1 == 1 and alpha.shape == gates and alpha.dtype is torch.float32 and alpha.get_device() == i
-        if beta is not None:
-            br, b1 = beta.stride()
-            bp = beta.data_ptr()
-            fits = fits and b1 == 1 and beta.shape == gates and beta.dtype is torch.float32 and beta.get_device() == i
-        if cu_seqlens is not None:
-            S = cu_seqlens.shape[0] - 1
-            cp = cu_seqlens.data_ptr()
-            fits = fits and S >= 0 and cu_seqlens.dtype is torch.int32 and cu_seqlens.stride() == (1,) and cu_seqlens.get_device() == i
-        if slots is not None:
-            sp = slots.data_ptr()
-            fits = fits and slots.shape == (S,) and slots.dtype is torch.int32 and slots.stride() == (1,) and slots.get_device() == i
-        if out is not None:
-            od = out.dtype
-            fits = fits and out.shape == (N, H, dv) and (o_dtype is None or od is o_dtype) and out.get_device() == i and out.is_contiguous()
-        else:
-            od = o_dtype or io
-        if torch.is_grad_enabled():
-            fits = fits and not any(t is not None and t.requires_grad for t in (q, k, v, alpha, beta, state, out))
-        fits = fits and io in _DTYPES and od in _DTYPES
-    except (AttributeError, TypeError, ValueError, IndexError):
-        fits = False
-    if not fits:
-        _recurrent_refuse(q, k, v, alpha, beta, state, slots, cu_seqlens, o_dtype, out)
-    if out is None:
-        dev = q.device
-        out = _empty((N, H, dv), (H * dv, dv, 1), device=dev, dtype=od) if cu_seqlens is None else torch.zeros((N, H, dv), device=dev, dtype=od)
-    _launch("gdn_recurrent_fwd", _pack_recurrent(
-        N, S, H, Hk, dk, dv, P, _DTYPES[io], _DTYPES[od], 0 if qk_norm_eps is None else 1, qk_norm_eps or 0.0,
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), qr, qh, kr, kh, vr, vh, ap, bp, ar, br, cp, sp, state.data_ptr(),
-        out.data_ptr()), i)
-    return out
-
-
-def _recurrent_refuse(q, k, v, alpha, beta, state, slots, cu_seqlens, o_dtype, out):
-    """Raises for what recurrent_fwd does not take; returns where only its quick test was too
-    strict (a dimension of one element with some other stride)."""
     _tensors(q=q, k=k, v=v, state=state)
     if q.dim() != 3 or v.dim() != 3 or state.dim() != 4:
         raise ValueError("q must be [N, Hk, dk], v [N, H, dv] and state [P, H, dk, dv]")
     _first(q, "q", 3, _IO)
-    dev, (N, _, dk), (_, H, dv), S = q.device, q.shape, v.shape, q.shape[0]
-    _check(k, "k", q.shape, (q.dtype,), dev)
-    _check(v, "v", (N, H, dv), (q.dtype,), dev)
-    _check(state, "state", (state.shape[0], H, dk, dv), _F32, dev)
-    if alpha is not None:
-        _check(alpha, "alpha", (N, H), _F32, dev)
-    if beta is not None:
-        _check(beta, "beta", (N, H), _F32, dev)
+    dev, io, (N, Hk, dk), (_, H, dv), P, S = q.device, q.dtype, q.shape, v.shape, state.shape[0], q.shape[0]
+    _check(k, "k", q.shape, (io,), dev)
+    _check(v, "v", (N, H, dv), (io,), dev)
+    _check(state, "state", (P, H, dk, dv), _F32, dev)
+    if not state.is_contiguous():
+        raise ValueError("state must be contiguous")
+    for t, name in ((alpha, "alpha"), (beta, "beta")):
+        if t is not None:
+            _check(t, name, (N, H), _F32, dev)
     if cu_seqlens is not None:
         _tensors(cu_seqlens=cu_seqlens)
         if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
@@ -295,37 +251,36 @@ def _recurrent_refuse(q, k, v, alpha, beta, state, slots, cu_seqlens, o_dtype, o
         _check(cu_seqlens, "cu_seqlens", (S + 1,), _I32, dev)
     if slots is not None:
         _check(slots, "slots", (S,), _I32, dev)
-    if not state.is_contiguous():
-        raise ValueError("state must be contiguous")
-    _code(q.dtype), _code(o_dtype or q.dtype)
     if out is not None:
         _tensors(out=out)
         _check(out, "out", (N, H, dv), (o_dtype or out.dtype,), dev)
-        _code(out.dtype)
         if not out.is_contiguous():
             raise ValueError("out must be contiguous")
+    od = out.dtype if out is not None else o_dtype or io
+    code = _code(od)
+    if out is None:
+        out = (torch.empty if cu_seqlens is None else torch.zeros)((N, H, dv), device=dev, dtype=od)
+    row = lambda t: 0 if t is None else t.stride(0)  # noqa: E731
+    _launch("gdn_recurrent_fwd", _pack_recurrent(
+        N, S, H, Hk, dk, dv, P, _DTYPES[io], code, 0 if qk_norm_eps is None else 1, qk_norm_eps or 0.0,
+        _ptr(q), _ptr(k), _ptr(v), *q.stride()[:2], *k.stride()[:2], *v.stride()[:2], _ptr(alpha), _ptr(beta), row(alpha), row(beta),
+        _ptr(cu_seqlens), _ptr(slots), _ptr(state), _ptr(out)), dev.index)
+    return out
 
 
-def _tensors(**named):
-    for name in named:
-        if not isinstance(named[name], torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
-
-
-def _code(dt):
-    if dt not in _DTYPES:
-        raise TypeError(f"unsupported dtype {dt}; use torch.bfloat16 or torch.float32")
-    return _DTYPES[dt]
-
-
-def _steps(lead, rows, width, dev):
+def _steps(lead, width, dev):
     """Rows of int8 [*lead, width] that start on 16 bytes, their stride, and their scales [*lead]."""
     pitch = (width + 15) // 16 * 16
-    if len(lead) == 1:
-        return (_empty((rows, width), (pitch, 1), device=dev, dtype=torch.int8), pitch,
-                _empty((rows,), (1,), device=dev, dtype=torch.float32))
     q = torch.empty((*lead, pitch), device=dev, dtype=torch.int8)
     return q if pitch == width else q[..., :width], pitch, torch.empty(lead, device=dev, dtype=torch.float32)
+
+
+def _weight(weight, shape, dev):
+    """(dtype code, address) of a norm's weight."""
+    if weight is None:
+        return 0, 0
+    _check(weight, "weight", shape, _IO, dev)
+    return _DTYPES[weight.dtype], weight.data_ptr()
 
 
 def add_rms_norm_int8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None, *,
@@ -346,65 +301,24 @@ def add_rms_norm_int8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, re
     r = (_quick or _bind_quick()).add_rms_norm_int8(x, weight, residual, eps, residual_out)
     if r is not None:
         return r if type(r) is not int else _failed(r)
-    i, grad, xd = _row_input(x, 1)
-    shape, dev = x.shape, x.device
-    flat = len(shape) == 2
-    rows, xr = (shape[0], x.stride()[0]) if flat else _rows(x, "x")
-    D = shape[-1]
-    rr = ror = rdt = wdt = wp = rp = rop = 0
-    if weight is not None:
-        wdt, wp = _row_weight(weight, (D,), i, grad, dev)
+    _first(x, "x", 1, _IO)
+    shape, dev, D = x.shape, x.device, x.shape[-1]
+    rows, xr = _rows(x, "x")
+    wdt, wp = _weight(weight, (D,), dev)
+    rr = ror = rdt = 0
     if residual is not None:
-        try:
-            rd, (rr, r1) = residual.dtype, residual.stride()
-            fits = flat and r1 == 1 and residual.shape == shape and rd in _DTYPES and residual.get_device() == i and not (grad and residual.requires_grad)
-        except (AttributeError, ValueError):
-            fits = False
-        if not fits:
-            _tensors(residual=residual)
-            _check(residual, "residual", shape, _IO, dev)
-            rd, rr = residual.dtype, _rows(residual, "residual")[1]
-        rdt, rp = _DTYPES[rd], residual.data_ptr()
+        _check(residual, "residual", shape, _IO, dev)
+        rdt, rr = _DTYPES[residual.dtype], _rows(residual, "residual")[1]
         if residual_out is None:
-            residual_out = _empty(shape, (D, 1), device=dev, dtype=rd) if flat else torch.empty(shape, device=dev, dtype=rd)
-            ror = D
-        else:
-            _tensors(residual_out=residual_out)
-            _check(residual_out, "residual_out", shape, (rd,), dev)
-            ror = _rows(residual_out, "residual_out")[1]
-        rop = residual_out.data_ptr()
+            residual_out = torch.empty(shape, device=dev, dtype=residual.dtype)
+        _check(residual_out, "residual_out", shape, (residual.dtype,), dev)
+        ror = _rows(residual_out, "residual_out")[1]
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
-    q, qr, scale = _steps(shape[:-1], rows, D, dev)
-    _launch("gdn_rows_int8", _pack_rows(ROWS_NORM, rows, D, 0, xd, rdt, wdt, eps, x.data_ptr(), rp, 0, wp, xr, rr, 0, ror, qr,
-                                        rop, q.data_ptr(), scale.data_ptr()), i)
+    q, qr, scale = _steps(shape[:-1], D, dev)
+    _launch("gdn_rows_int8", _pack_rows(ROWS_NORM, rows, D, 0, _DTYPES[x.dtype], rdt, wdt, eps, _ptr(x), _ptr(residual), 0, wp, xr, rr, 0,
+                                        ror, qr, _ptr(residual_out), _ptr(q), _ptr(scale)), dev.index)
     return q, scale, residual_out
-
-
-def _row_input(x, dims):
-    """(device index, whether gradients are recorded, dtype code) of a checked x."""
-    grad = torch.is_grad_enabled()
-    try:
-        i, xd, stride = x.get_device(), _DTYPES.get(x.dtype), x.stride()
-        fits = xd is not None and i >= 0 and len(stride) >= dims and stride[-1] == 1 and not (grad and x.requires_grad)
-    except AttributeError:
-        fits = False
-    if not fits:
-        _first(x, "x", dims, _IO)
-    return i, grad, xd
-
-
-def _row_weight(weight, shape, i, grad, dev):
-    try:
-        wd = weight.dtype
-        fits = (wd in _DTYPES and weight.shape == shape and weight.stride() == (1,) and weight.get_device() == i
-                and not (grad and weight.requires_grad))
-    except AttributeError:
-        fits = False
-    if not fits:
-        _tensors(weight=weight)
-        _check(weight, "weight", shape, _IO, dev)
-    return _DTYPES[weight.dtype], weight.data_ptr()
 
 
 def _head_rows(t, name):
@@ -434,26 +348,15 @@ def gated_rms_norm_int8(x: torch.Tensor, gate: torch.Tensor, weight: Optional[to
     r = (_quick or _bind_quick()).gated_rms_norm_int8(x, gate, weight, eps)
     if r is not None:
         return r if type(r) is not int else _failed(r)
-    i, grad, xd = _row_input(x, 2)
-    dev = x.device
-    shape = x.shape
-    *lead, H, d = shape
-    try:
-        fits = (gate.shape == shape and gate.dtype is x.dtype and gate.get_device() == i and gate.stride()[-1] == 1
-                and not (grad and gate.requires_grad))
-    except AttributeError:
-        fits = False
-    if not fits:
-        _tensors(gate=gate)
-        _check(gate, "gate", shape, (x.dtype,), dev)
-    wdt = wp = 0
-    if weight is not None:
-        wdt, wp = _row_weight(weight, (d,), i, grad, dev)
+    _first(x, "x", 2, _IO)
+    dev, (*lead, H, d) = x.device, x.shape
+    _check(gate, "gate", x.shape, (x.dtype,), dev)
+    wdt, wp = _weight(weight, (d,), dev)
     rows, xr = _head_rows(x, "x")
     gr = _head_rows(gate, "gate")[1]
-    q, qr, scale = _steps(lead, rows, H * d, dev)
-    _launch("gdn_rows_int8", _pack_rows(ROWS_GATED, rows, H * d, d, xd, 0, wdt, eps, x.data_ptr(), 0, gate.data_ptr(), wp, xr,
-                                        0, gr, 0, qr, 0, q.data_ptr(), scale.data_ptr()), i)
+    q, qr, scale = _steps(lead, H * d, dev)
+    _launch("gdn_rows_int8", _pack_rows(ROWS_GATED, rows, H * d, d, _DTYPES[x.dtype], 0, wdt, eps, _ptr(x), 0, _ptr(gate), wp, xr,
+                                        0, gr, 0, qr, 0, _ptr(q), _ptr(scale)), dev.index)
     return q, scale
 
 
@@ -466,12 +369,11 @@ def quantize_int8(x: torch.Tensor, *, stream: Optional[torch.cuda.Stream] = None
     r = (_quick or _bind_quick()).quantize_int8(x)
     if r is not None:
         return r if type(r) is not int else _failed(r)
-    i, _, xd = _row_input(x, 1)
-    D = x.shape[-1]
-    rows, xr = _rows(x, "x")
-    q, qr, scale = _steps(x.shape[:-1], rows, D, x.device)
-    _launch("gdn_rows_int8", _pack_rows(ROWS_PLAIN, rows, D, 0, xd, 0, 0, 0.0, x.data_ptr(), 0, 0, 0, xr, 0, 0, 0, qr, 0,
-                                        q.data_ptr(), scale.data_ptr()), i)
+    _first(x, "x", 1, _IO)
+    D, (rows, xr) = x.shape[-1], _rows(x, "x")
+    q, qr, scale = _steps(x.shape[:-1], D, x.device)
+    _launch("gdn_rows_int8", _pack_rows(ROWS_PLAIN, rows, D, 0, _DTYPES[x.dtype], 0, 0, 0.0, _ptr(x), 0, 0, 0, xr, 0, 0, 0, qr, 0,
+                                        _ptr(q), _ptr(scale)), x.device.index)
     return q, scale
 
 
@@ -490,65 +392,27 @@ def int8_matmul(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale
     r = (_quick or _bind_quick()).int8_matmul(x, x_scale, w, w_scale, bias, out_dtype, out)
     if r is not None:
         return r if type(r) is not int else _failed(r)
-    grad = torch.is_grad_enabled()
-    try:
-        shape, i = x.shape, x.get_device()
-        lead, K = shape[:-1], shape[-1]
-        N, wk = w.shape
-        wr, w1 = w.stride()
-        fits = (i >= 0 and x.dtype is torch.int8 and x.stride()[-1] == 1 and wk == K and w1 == 1 and w.dtype is torch.int8
-                and w.get_device() == i and w_scale.shape == (N,) and w_scale.dtype is torch.float32 and w_scale.stride() == (1,)
-                and w_scale.get_device() == i and x_scale.shape == lead and x_scale.dtype is torch.float32
-                and x_scale.get_device() == i and x_scale.is_contiguous() and not (grad and (x_scale.requires_grad or w_scale.requires_grad)))
-    except (AttributeError, TypeError, ValueError, IndexError):
-        fits = False
-    dev = x.device if fits else _product_refuse(x, x_scale, w, w_scale)
-    bp = 0
-    if bias is not None:
-        _tensors(bias=bias)
-        if not (bias.shape == (N,) and bias.dtype is torch.float32 and bias.stride() == (1,) and bias.get_device() == i and not (grad and bias.requires_grad)):
-            _check(bias, "bias", (N,), _F32, dev)
-        bp = bias.data_ptr()
-    M, xr = _rows(x, "x")
-    od = _code(out_dtype)
-    if out is None:
-        out = _empty((M, N), (N, 1), device=dev, dtype=out_dtype) if len(lead) == 1 else torch.empty((*lead, N), device=dev, dtype=out_dtype)
-        outr = N
-    else:
-        _tensors(out=out)
-        _check(out, "out", (*lead, N), (out_dtype,), dev)
-        outr = _rows(out, "out")[1]
-    xp, wp = x.data_ptr(), w.data_ptr()
-    fields = (M, N, K, od, xp, wp, xr, wr, outr, x_scale.data_ptr(), w_scale.data_ptr(), bp, out.data_ptr())
-    ws = need = 0
-    if (xp | wp | xr | wr) & 15 or not xr or not wr:
-        # from torch's allocator and not kept: a call's copies belong to its stream, or its graph
-        need = lib().gdn_int8_matmul_workspace_bytes(_pack_matmul(*fields, 0, 0))
-        if need:
-            buffer = _empty((need,), (1,), device=dev, dtype=torch.uint8)
-            ws = buffer.data_ptr()
-    _launch("gdn_int8_matmul", _pack_matmul(*fields, ws, need), i)
-    return out
-
-
-def _product_refuse(x, x_scale, w, w_scale):
-    """Raises for what int8_matmul does not take; the device where only its quick test was too
-    strict."""
     _tensors(x=x, x_scale=x_scale, w=w, w_scale=w_scale)
     if w.dim() != 2:
         raise ValueError("w must be [N, K]")
     _first(x, "x", 1, _I8)
-    _check(w, "w", (w.shape[0], x.shape[-1]), _I8, x.device)
-    _check(w_scale, "w_scale", (w.shape[0],), _F32, x.device)
-    _check_scale(x_scale, x.shape[:-1], x.device)
-    return x.device
-
-
-def _check_scale(t, lead, dev):
-    if not t.is_contiguous():
+    dev, (*lead, K), N = x.device, x.shape, w.shape[0]
+    _check(w, "w", (N, K), _I8, dev)
+    _check(w_scale, "w_scale", (N,), _F32, dev)
+    if not x_scale.is_contiguous():
         raise ValueError("x_scale must be contiguous")
-    if t.dim() == 0:
-        if len(lead):
-            raise ValueError(f"x_scale has shape (), expected {tuple(lead)}")
-        t, lead = t.view(1), (1,)
-    _check(t, "x_scale", lead, _F32, dev)
+    _check(x_scale, "x_scale", tuple(lead), _F32, dev)
+    if bias is not None:
+        _check(bias, "bias", (N,), _F32, dev)
+    od = _code(out_dtype)
+    if out is None:
+        out = torch.empty((*lead, N), device=dev, dtype=out_dtype)
+    _check(out, "out", (*lead, N), (out_dtype,), dev)
+    M, xr = _rows(x, "x")
+    outr = _rows(out, "out")[1]
+    fields = (M, N, K, od, _ptr(x), _ptr(w), xr, w.stride(0), outr, _ptr(x_scale), _ptr(w_scale), _ptr(bias), _ptr(out))
+    need = lib().gdn_int8_matmul_workspace_bytes(_pack_matmul(*fields, 0, 0))
+    # from torch's allocator and not kept: a call's copies belong to its stream, or its graph
+    workspace = torch.empty(need, device=dev, dtype=torch.uint8) if need else None
+    _launch("gdn_int8_matmul", _pack_matmul(*fields, _ptr(workspace), need), dev.index)
+    return out

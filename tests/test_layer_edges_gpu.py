@@ -240,3 +240,58 @@ def test_other_threads_run_while_a_call_waits(tmp_path):
         gdn.layer._bind_quick()
     assert type(_layer.quantize_int8(x)) is tuple
     gdn.device_check()
+
+
+@pytest.mark.parametrize("quick", [True, False])
+def test_rows_of_any_leading_dimensions(quick, monkeypatch):
+    """One row, batches of rows, strides that are one run, dimensions of one, and rows that are not
+    one run, through the quick binding and without it; the same numbers as of plain rows."""
+    import chunked_gated_delta_14_b200.layer as L
+    long_way = []
+    if quick:
+        launch = L._launch
+        monkeypatch.setattr(L, "_launch", lambda *a: (long_way.append(a), launch(*a)))
+    else:
+        monkeypatch.setattr(L, "_quick", L._NoQuick)
+    g = rng(87)
+    wide = randn(g, 6, 4, 300)
+    w = 1 + 0.1 * randn(g, 100)
+    wq, ws = gdn.quantize_int8(randn(g, 40, 100))
+    for io in (BF, F):
+        for x in (wide[:, :, 3:103], wide[1, :, :100], wide[1, 2, 7:107], wide[:, None, 2:3, :100], wide[::2, 1:2, :100], wide[None, 3, 1:2, None, :100]):
+            x = x.to(io) if x.is_contiguous() else torch.empty_strided(x.shape, x.stride(), device="cuda", dtype=io).copy_(x)
+            flat = x.reshape(-1, 100).clone()
+            lead = x.shape[:-1]
+            for got, want in ((gdn.quantize_int8(x), gdn.quantize_int8(flat)),
+                              (gdn.add_rms_norm_int8(x, w, x), gdn.add_rms_norm_int8(flat, w, flat)),
+                              (gdn.add_rms_norm_int8(x, w, eps=1), gdn.add_rms_norm_int8(flat, w, eps=1.0))):
+                assert got[0].shape == x.shape and got[1].shape == lead and got[0].stride(-1) == 1
+                assert not lead or got[0].stride(-2) == 112 and got[0].data_ptr() % 16 == 0
+                assert torch.equal(got[0].reshape(-1, 100), want[0]) and torch.equal(got[1].reshape(-1), want[1])
+                if len(got) == 3 and want[2] is not None:
+                    assert got[2].shape == x.shape and torch.equal(got[2].reshape(-1, 100), want[2])
+            r = x.clone()
+            q, s, h = gdn.add_rms_norm_int8(x, w, r, residual_out=r)
+            assert h is r and torch.equal(h, (x + x)) and q.shape == x.shape
+            out = gdn.int8_matmul(q, s, wq, ws, out_dtype=F)
+            assert out.shape == (*lead, 40) and torch.equal(out.reshape(-1, 40), gdn.int8_matmul(q.reshape(-1, 100), s.reshape(-1), wq, ws, out_dtype=F))
+            place = torch.full((*lead, 48), 5.0, device="cuda")[..., :40]
+            assert gdn.int8_matmul(q, s, wq, ws, out_dtype=F, out=place) is place and torch.equal(place, out)
+            if len(lead):
+                y = x.unflatten(-1, (5, 20))[..., :16].contiguous()
+                q, s = gdn.gated_rms_norm_int8(y, y)
+                q2, s2 = gdn.gated_rms_norm_int8(y.view(-1, 5, 16), y.view(-1, 5, 16))
+                assert q.shape == (*lead, 80) and torch.equal(q.reshape(-1, 80), q2) and torch.equal(s.reshape(-1), s2)
+    gdn.gated_rms_norm_int8(randn(g, 3, 16), randn(g, 3, 16))
+    assert not long_way
+    for x in (wide[:, :3, :100], wide.transpose(0, 1)[..., :100]):         # not one run
+        with pytest.raises(ValueError, match="one run"):
+            gdn.quantize_int8(x)
+    assert gdn.quantize_int8(wide[:0])[0].shape == (0, 4, 300)
+    assert gdn.int8_matmul(wq.view(2, 20, 100)[:, :0], ws.view(2, 20)[:, :0], wq, ws).shape == (2, 0, 40)
+    with pytest.raises(ValueError):
+        gdn.add_rms_norm_int8(wide[0], None, wide[0, :3])
+    with pytest.raises(gdn.GDNError, match="overlap"):
+        gdn.add_rms_norm_int8(wide[:1].expand(3, 4, 300).reshape(12, 300)[:2], None, wide[0, :2].clone(),
+                              residual_out=wide[5, 3:].expand(2, 300))
+    gdn.device_check()
