@@ -9,6 +9,7 @@
 // The checks that keep a call in bounds are the library's own, in both ways.
 #include <Python.h>
 #include <ATen/ATen.h>
+#include <c10/core/AutogradState.h>
 #include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -28,14 +29,16 @@ decltype(&gdn_int8_matmul_workspace_bytes) matmul_workspace_fn;
 // What a call's tensors have in common, and whether all of them fit so far.
 struct Call {
     int device = -1;
-    bool grad = c10::GradMode::is_enabled();
+    bool grad = c10::GradMode::is_enabled(), tangents = c10::AutogradState::get_tls_state().get_fw_grad_mode();
     bool fits = true;
 
-    // A plain tensor on the call's device, with `least` dimensions or more, contiguous in the last.
+    // A plain tensor on the call's device, with `least` dimensions or more, contiguous in the last,
+    // and no derivative asked of it (a tangent's level is 0, the only one there is).
     const at::Tensor *any(PyObject *o, int64_t least) {
         if (!fits || !THPVariable_CheckExact(o)) { fits = false; return nullptr; }
         const at::Tensor &t = THPVariable_Unpack(o);
-        if (!t.is_cuda() || t.layout() != at::kStrided || t.dim() < least || (t.dim() && t.stride(-1) != 1) || (grad && t.requires_grad())) {
+        if (!t.is_cuda() || t.layout() != at::kStrided || t.dim() < least || (t.dim() && t.stride(-1) != 1) || (grad && t.requires_grad()) ||
+            (tangents && t._fw_grad(0).defined())) {
             fits = false;
             return nullptr;
         }

@@ -7,7 +7,7 @@ around the recurrence when it serves.
 Argument marshalling only, as in gdn.py.  Every call is asynchronous on the
 device's current stream (or ``stream``), takes tensors whose last dimension is
 contiguous, and serves inference: an input that requires a gradient is refused
-while gradients are recorded.
+while gradients are recorded, and one that carries a tangent (forward mode).
 """
 from __future__ import annotations
 
@@ -16,6 +16,7 @@ import struct
 from typing import Optional, Tuple
 
 import torch
+from torch.autograd import forward_ad
 
 from .build import binding_for
 from .gdn import GDN_BF16, GDN_F32, GDN_OK, GDNError, last_error, lib
@@ -106,6 +107,8 @@ def _check(t, name, shape, dtypes, device):
         raise TypeError(f"{name} has dtype {t.dtype}, expected " + " or ".join(map(str, dtypes)))
     if t.requires_grad and torch.is_grad_enabled():
         raise ValueError(f"{name} requires a gradient: the decode-layer operators have none")
+    if forward_ad._current_level >= 0 and forward_ad.unpack_dual(t).tangent is not None:
+        raise ValueError(f"{name} carries a tangent: the decode-layer operators have no derivatives")
     if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
     if any(n > 2 ** 31 - 1 for n in t.shape):

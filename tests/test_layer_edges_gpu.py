@@ -295,3 +295,24 @@ def test_rows_of_any_leading_dimensions(quick, monkeypatch):
         gdn.add_rms_norm_int8(wide[:1].expand(3, 4, 300).reshape(12, 300)[:2], None, wide[0, :2].clone(),
                               residual_out=wide[5, 3:].expand(2, 300))
     gdn.device_check()
+
+
+@pytest.mark.parametrize("quick", [True, False])
+def test_tangents_are_refused_in_every_argument(quick, monkeypatch):
+    import torch.autograd.forward_ad as fw
+    import chunked_gated_delta_14_b200.layer as L
+    if not quick:
+        monkeypatch.setattr(L, "_quick", L._NoQuick)
+    x, i8, s = torch.ones(4, 64, device="cuda"), torch.ones(4, 64, device="cuda", dtype=torch.int8), torch.ones(4, device="cuda")
+    w, q, state, a = torch.ones(64, device="cuda"), x.view(4, 1, 64), torch.zeros(4, 1, 64, 64, device="cuda"), torch.ones(4, 1, device="cuda")
+    calls = [(gdn.quantize_int8, [x]), (gdn.add_rms_norm_int8, [x, w, x]), (gdn.gated_rms_norm_int8, [x.view(4, 2, 32), x.view(4, 2, 32), w[:32]]),
+             (gdn.int8_matmul, [i8, s, i8, s, s]), (gdn.recurrent_fwd, [q, q, q, a, a, state])]
+    with fw.dual_level():
+        for f, args in calls:
+            for i, t in enumerate(args):
+                if t.is_floating_point():
+                    dual = fw.make_dual(t, torch.ones_like(t))
+                    with torch.no_grad(), pytest.raises(ValueError, match="tangent"):
+                        f(*args[:i], dual, *args[i + 1:])
+            f(*args)                                 # the same without
+    gdn.device_check()
