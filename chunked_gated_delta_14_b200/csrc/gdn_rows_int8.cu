@@ -437,6 +437,7 @@ __global__ void __launch_bounds__(MOST) gated_kernel(const RowsParams p, int lan
             widen<float>(ww, w);
         }
     }
+    times(w, 0x1p-32f);
     F2 y[V][4];
     float norm[V], top = 0.f;
 #pragma unroll
@@ -469,20 +470,23 @@ __global__ void __launch_bounds__(MOST) gated_kernel(const RowsParams p, int lan
     }
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        F2 gate[4];
+        F2 gate[4], one[4];
         widen<XT>(gw[j], gate);
-        // g / (1 + e^-g): an approximate exponential and quotient, off by some 2^-22 of the
-        // result for |g| < 20 (an error of the exponent counts |g| times), against steps of 2^-7
+        // g / (1 + e^-g): an approximate exponential and reciprocal, off by some 2^-22 of the
+        // result for |g| < 20 (an error of the exponent counts |g| times), against steps of 2^-7.
+        // The sum is formed 2^-32 times, and w holds the rest, so that its reciprocal is a normal
+        // number for every g whose product may be one.
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             float lo, hi;
-            unpack(mul2(gate[e], pack(-1.44269504f, -1.44269504f)), &lo, &hi);
-            unpack(add2(pack(sm100::ex2_approx(lo), sm100::ex2_approx(hi)), pack(1.f, 1.f)), &lo, &hi);
-            gate[e] = mul2(gate[e], pack(rcp(lo), rcp(hi)));
+            unpack(fma2(gate[e], pack(-1.44269504f, -1.44269504f), pack(-32.f, -32.f)), &lo, &hi);
+            unpack(add2(pack(sm100::ex2_approx(lo), sm100::ex2_approx(hi)), pack(0x1p-32f, 0x1p-32f)), &lo, &hi);
+            one[e] = pack(rcp(lo), rcp(hi));
         }
         times(y[j], norm[j]);
         times(y[j], w);
         times(y[j], gate);
+        times(y[j], one);
         top = top_of(top, y[j]);
     }
     const Totals t = row_totals<false>(0.f, top);

@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import chunked_gated_delta_14_b200 as gdn
-from test_layer_gpu import BF, F, check_product, check_rows, check_rule, make_product, make_rule, randn, rng, rows_x, rule64
+from test_layer_gpu import BF, F, U, check_product, check_rows, check_rule, make_product, make_rule, randn, rng, rows_x, rule64
 
 pytestmark = pytest.mark.gpu
 
@@ -316,3 +316,22 @@ def test_tangents_are_refused_in_every_argument(quick, monkeypatch):
                         f(*args[:i], dual, *args[i + 1:])
             f(*args)                                 # the same without
     gdn.device_check()
+
+
+@pytest.mark.parametrize("io", [BF, F])
+@pytest.mark.parametrize("lo,hi,weight", [(-90, -80, 1.0), (-88.6, -87.4, 1.0), (-95, -86, 1e4), (-100, 100, 1e4), (60, 100, 1.0)])
+def test_gated_of_gates_far_below_zero(lo, hi, weight, io):
+    """silu there is g e^g, small, but its rows have a scale.  The exponent is rounded once, to half
+    of 2^-17 below 128, and its factor log2(e) is off by 0.23 u of it: 44 u + 21 u of the result; with
+    the exponential's and the quotient's 2 units in the last place each and check_rows' 32 u: 110 u."""
+    g = rng(88)
+    x, gate = randn(g, 50, 4, 64).to(io), (lo + (hi - lo) * torch.rand(50, 4, 64, device="cuda", generator=g)).to(io)
+    w = weight * (1 + 0.2 * randn(g, 64))
+    q, scale = gdn.gated_rms_norm_int8(x, gate, w)
+    xd, gd = x.double(), gate.double()
+    y = (xd / (xd.pow(2).mean(-1, keepdim=True) + 1e-6).sqrt() * w.double() * gd * torch.sigmoid(gd)).flatten(1)
+    want = y.abs().amax(1) / 127
+    assert want.min() > 2.0 ** -126
+    assert ((scale.double() - want).abs() <= 110 * U * want).all(), float(((scale.double() - want).abs() / want).max() / U)
+    assert ((q.double() - y / want[:, None]).abs() <= 0.5 + 127 * 250 * U).all()
+    assert (q.abs().amax(1) == 127).all()
