@@ -1,10 +1,12 @@
 """Decode-layer operators: what can be held without a GPU, beside the refusals."""
 import os
 import subprocess
+import sys
 
 import pytest
 import torch
 
+import bench
 import chunked_gated_delta_14_b200 as gdn
 import chunked_gated_delta_14_b200.layer as L
 from chunked_gated_delta_14_b200 import build as gbuild
@@ -94,3 +96,15 @@ def test_library_builds_without_a_host_compiler_for_the_binding(binding_elsewher
     monkeypatch.setenv("CXX", cxx)
     assert gbuild.build() == gbuild.LIB and os.path.exists(gbuild.LIB)
     assert "not built" in capsys.readouterr().err and not gbuild.binding_is_current()
+
+
+def test_bench_says_what_the_layer_finds_in_l2():
+    assert "> 126 MB" in bench.layer_l2(256, 16, 128)
+    assert "stay in" in bench.layer_l2(4, 16, 128)
+
+
+def test_bench_refuses_the_layer_without_decode(monkeypatch, capsys):
+    monkeypatch.setattr(sys, "argv", ["bench.py", "--layer"])
+    with pytest.raises(SystemExit) as e:
+        bench.main()
+    assert e.value.code == 2 and "--decode" in capsys.readouterr().err
