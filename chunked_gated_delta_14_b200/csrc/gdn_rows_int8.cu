@@ -4,19 +4,20 @@
 //   PLAIN  y = x
 //   NORM   h = x + residual,  y = h rsqrt(mean h^2 + eps) w
 //   GATED  y = x rsqrt(mean over the head of x^2 + eps) w gate / (1 + e^-gate)
-//   scale = max|y| / 127,  q = rint(y 127 / max|y|)
+//   scale = max|y| / 127,  q = rint(127 y / max|y|)
 //
 // Bound by memory: a row is read once, stays in registers (8 V numbers a thread)
 // while its statistics go round the row's threads, and is written once.  The
 // largest |h w| is found beside the sum of squares, since the norm's factor is
-// positive and the same for the whole row, so NORM too has one exchange.  Beside
-// the bytes the instructions count (bf16 rows leave about 20 a number): everything
-// is loaded before anything is waited for, products and sums go two in an
-// instruction, and steps come from a sum instead of a conversion.
+// positive and the same for the whole row, so NORM too has one exchange (a second one
+// where the squares pass fp32).  Beside the bytes the instructions count (bf16 rows
+// leave about 20 a number): everything is loaded before anything is waited for,
+// products and sums go two in an instruction, and steps come from an fma instead of a
+// conversion.
 //
-// Measured, of the copy rate: NORM of 8192 x 4096 bf16 with an fp32 residual 57 us
-// (98%); PLAIN of 8224 x 2048 bf16 8.0 us (97%); GATED of 16384 rows of 16 heads of
-// 128 31 us (82%: an exponential and a reciprocal a number).
+// Measured, of the copy rate: NORM of 8192 x 4096 bf16 with an fp32 residual 58 us
+// (98%); PLAIN of 8224 x 2048 bf16 8.3 us (93%); GATED of 16384 rows of 16 heads of
+// 128 32 us (79%: an exponential and a reciprocal a number, 3.0 instructions a cycle).
 #include <cuda_bf16.h>
 
 #include <type_traits>
@@ -437,7 +438,7 @@ __global__ void __launch_bounds__(MOST) gated_kernel(const RowsParams p, int lan
             widen<float>(ww, w);
         }
     }
-    times(w, 0x1p-32f);
+    times(w, 0x1p-12f);
     F2 y[V][4];
     float norm[V], top = 0.f;
 #pragma unroll
@@ -474,13 +475,13 @@ __global__ void __launch_bounds__(MOST) gated_kernel(const RowsParams p, int lan
         widen<XT>(gw[j], gate);
         // g / (1 + e^-g): an approximate exponential and reciprocal, off by some 2^-22 of the
         // result for |g| < 20 (an error of the exponent counts |g| times), against steps of 2^-7.
-        // The sum is formed 2^-32 times, and w holds the rest, so that its reciprocal is a normal
-        // number for every g whose product may be one.
+        // The sum is formed 2^-12 times, and w brings the rest back, so that its reciprocal is a
+        // normal number down to g = -95 (-87 without); there silu is 1e-39, below any scale.
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             float lo, hi;
-            unpack(fma2(gate[e], pack(-1.44269504f, -1.44269504f), pack(-32.f, -32.f)), &lo, &hi);
-            unpack(add2(pack(sm100::ex2_approx(lo), sm100::ex2_approx(hi)), pack(0x1p-32f, 0x1p-32f)), &lo, &hi);
+            unpack(fma2(gate[e], pack(-1.44269504f, -1.44269504f), pack(-12.f, -12.f)), &lo, &hi);
+            unpack(add2(pack(sm100::ex2_approx(lo), sm100::ex2_approx(hi)), pack(0x1p-12f, 0x1p-12f)), &lo, &hi);
             one[e] = pack(rcp(lo), rcp(hi));
         }
         times(y[j], norm[j]);

@@ -319,7 +319,7 @@ def test_tangents_are_refused_in_every_argument(quick, monkeypatch):
 
 
 @pytest.mark.parametrize("io", [BF, F])
-@pytest.mark.parametrize("lo,hi,weight", [(-90, -80, 1.0), (-88.6, -87.4, 1.0), (-95, -86, 1e4), (-100, 100, 1e4), (60, 100, 1.0)])
+@pytest.mark.parametrize("lo,hi,weight", [(-90, -80, 1.0), (-88.6, -87.4, 1.0), (-95, -86, 1e4), (-100, 100, 1e4), (60, 100, 1.0), (-3, 3, 1e-33)])
 def test_gated_of_gates_far_below_zero(lo, hi, weight, io):
     """silu there is g e^g, small, but its rows have a scale.  The exponent is rounded once, to half
     of 2^-17 below 128, and its factor log2(e) is off by 0.23 u of it: 44 u + 21 u of the result; with
@@ -335,3 +335,51 @@ def test_gated_of_gates_far_below_zero(lo, hi, weight, io):
     assert ((scale.double() - want).abs() <= 110 * U * want).all(), float(((scale.double() - want).abs() / want).max() / U)
     assert ((q.double() - y / want[:, None]).abs() <= 0.5 + 127 * 250 * U).all()
     assert (q.abs().amax(1) == 127).all()
+
+
+@pytest.mark.parametrize("M,N,K,step", [(40, 30, 64, 16), (40, 30, 100, 48), (300, 200, 130, 32)])
+def test_product_of_rows_that_overlap(M, N, K, step):
+    g = rng(77)
+    make = lambda r: torch.randint(-128, 128, ((r - 1) * step + K,), device="cuda", generator=g, dtype=torch.int8).as_strided((r, K), (step, 1))  # noqa: E731
+    x, w = make(M), make(N)
+    xs, ws = torch.rand(M, device="cuda", generator=g), torch.rand(N, device="cuda", generator=g)
+    check_product(gdn.int8_matmul(x, xs, w, ws, out_dtype=F), x, xs, w, ws, None)
+
+
+def test_captured_over_two_streams():
+    """Operators on two streams of one capture, each launched right behind the other's event."""
+    x, xs, w, ws, _ = make_product(78, 20, 512, 256)
+    wu = w[:, 1:250]
+    a, r = rows_x(79, (20, 512), BF), rows_x(80, (20, 512), F)
+    q, k, v, al, be, state, starts = make_rule(81, [1] * 20, 2, 4, 64, 128)
+    lens = i32(starts)
+    s0 = state.clone()
+    side = torch.cuda.Stream()
+
+    def run(state):
+        main = torch.cuda.current_stream()
+        y = gdn.int8_matmul(x, xs, w, ws)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            z, zs, h = gdn.add_rms_norm_int8(y, None, r)
+            u = gdn.int8_matmul(z[:, :249], zs, wu[:, :249], ws)
+        o = gdn.recurrent_fwd(q, k, v, al, be, state, None, lens)
+        main.wait_stream(side)
+        p, ps = gdn.gated_rms_norm_int8(o, u.view(20, 4, 128))
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            t, ts = gdn.quantize_int8(h)
+        main.wait_stream(side)
+        return gdn.int8_matmul(p, ps, t, ts, out_dtype=F), o, u
+    want = run(s0)
+    torch.cuda.synchronize()
+    s1 = state.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run(s1)
+    for _ in range(3):
+        s1.copy_(state)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.equal(s1, s0)
+    gdn.device_check()
