@@ -264,9 +264,10 @@ __device__ __forceinline__ void store_few(float *p, const float (&x)[N]) {
 // are interleaved, so that the groups' 16-byte reads of k and q meet in no bank.
 // LONG: two fours between barriers, twice the registers, and the longest sequences
 // first.  NQ = 2 reads a token's k and q once for twice the columns, at 8 warps a SM
-// either way.  48 sequences of 0 to 600 tokens (5155 in all), 32 heads of 128 x 128:
-// 545 us (NQ = 1: 648); the fma's alone would take 225 (an f32x2 takes two cycles of
-// its pipe).
+// either way; at d_k 128 it spills a little of its 255 registers (132 bytes a thread in
+// bf16, 644 in fp32).  48 sequences of 0 to 600 tokens (5155 in all), 32 heads of
+// 128 x 128: 542 us (NQ = 1: 648); the fma's alone would take 225 (an f32x2 takes two
+// cycles of its pipe).
 template <int R, bool BF16, int W, bool LONG, int NQ>
 __global__ void __launch_bounds__(W * 32, R < 16 ? 1 : LONG ? 8 / W : 12 / W) recurrent_ragged_kernel(const PoolParams p) {
     if (p.early) { grid_next(); grid_wait(); }

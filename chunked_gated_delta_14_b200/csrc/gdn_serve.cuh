@@ -62,10 +62,12 @@ cudaError_t launch_int8_pad_rows(const PadRows &x, const PadRows &w, int K, cuda
 // kernel sets itself up, then waits (grid_wait) for that one's end before it reads or writes
 // anything outside itself, in every thread, so that its own end comes after that one's.
 // Back to back from the host a product of 16 rows takes 5.6 us so, 8.2 without, and a norm
-// of 16 x 2048 on the device 1.85 instead of 2.1.  Grids of more blocks than run at once begin
-// after that end as ever (but for the token step's equal blocks): taking the places of the last blocks one by one they were spread
-// worse (long ragged sequences 588 us instead of 545), and the wait alone, in each of 8224
-// blocks, cost plain rows of 2048 1.4 of 8 us.
+// of 16 x 2048 on the device 0.25 us less.  So the product and its copies at every size (with
+// copies of 1334 rows 8.8 us in a row of calls, 10.3 without; of 5001 rows 15.1, 18.6), the
+// one-token recurrence (its blocks are equal), and others of few blocks.  Of others, grids of
+// more blocks than run at once begin after that end as ever: taking the places of the last
+// blocks one by one they were spread worse (long ragged sequences 588 us instead of 545), and
+// the wait alone, in each of 8224 blocks, cost plain rows of 2048 1.4 of 8 us.
 inline bool is_early(unsigned blocks) { return blocks <= 296; }      // two an SM
 template <typename... A, typename... B>
 cudaError_t launch(bool early, void (*kernel)(A...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, unsigned cluster,

@@ -71,8 +71,8 @@ _quick = None
 
 
 def _bind_quick():
-    """_layer.so (csrc/layer_binding.cpp): the operators' calls of the usual form at a third of
-    the host's time.  What it does not take comes back as None and goes the long way below."""
+    """_layer.so (csrc/layer_binding.cpp): the operators' calls on plain tensors at a quarter of the
+    host's time.  What it does not take comes back as None and goes the long way below."""
     global _quick
     L = lib()
     try:
@@ -297,7 +297,8 @@ def add_rms_norm_int8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, re
     (bf16 or fp32; None = 1).  q: [..., D] int8, its rows on 16-byte boundaries; scale: [...]
     fp32, max|y| / 127; h: rounded to the residual's dtype, into ``residual_out`` if given
     (which may be ``residual``), None without a residual.  The norm takes h before that
-    rounding.  Rows of zeros have scale 0, rows with an infinity or a NaN scale NaN."""
+    rounding.  Rows of zeros have scale 0, rows with an infinity or a NaN scale NaN and
+    steps 0 (h * weight and y past fp32 are infinities)."""
     if stream is not None:
         return _other_stream(stream, x, (x, weight, residual, residual_out), lambda: add_rms_norm_int8(
             x, weight, residual, eps=eps, residual_out=residual_out))
@@ -344,8 +345,8 @@ def gated_rms_norm_int8(x: torch.Tensor, gate: torch.Tensor, weight: Optional[to
     and the rows of all heads in 8 bits.
 
     x, gate: [..., H, d] (bf16 or fp32, same dtype; the heads of a row adjacent, any row
-    stride), d a multiple of 8 up to 256; weight: [d] (bf16 or fp32; None = 1).  q: [..., H * d]
-    int8, its rows on 16-byte boundaries; scale: [...] fp32, one for all heads of a row."""
+    stride), d a multiple of 8 up to 256, H * d up to 32768 (H * (d / 8, rounded up to a power of
+    two) up to 4096); weight: [d] (bf16 or fp32; None = 1).  q: [..., H * d] int8, its rows on 16-byte boundaries; scale: [...] fp32, one for all heads of a row."""
     if stream is not None:
         return _other_stream(stream, x, (x, gate, weight), lambda: gated_rms_norm_int8(x, gate, weight, eps=eps))
     r = (_quick or _bind_quick()).gated_rms_norm_int8(x, gate, weight, eps)

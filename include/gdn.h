@@ -375,22 +375,23 @@ GDN_API gdn_status gdn_chunk_fwd_static_scratch(const gdn_fwd_args *args, void *
  * DeltaNet Quantizado" is about that layer; the pages print none of these
  * steps):
  *
- *   hidden -> gdn_add_rms_norm_int8 -> gdn_int8_matmul (q, k, v, gate, ...)
- *          -> gdn_recurrent_fwd -> gdn_gated_rms_norm_int8 -> gdn_int8_matmul
+ *   hidden -> gdn_rows_int8 (NORM) -> gdn_int8_matmul (q, k, v, gate, ...)
+ *          -> gdn_recurrent_fwd -> gdn_rows_int8 (GATED) -> gdn_int8_matmul
  *
  * Rows in 8 bits.  A row y of numbers is held as int8 steps and one fp32
- * scale: scale = max|y| / 127, step = y / scale rounded to nearest (ties to
+ * scale: scale = max|y| / 127, step = 127 y / max|y| rounded to nearest (ties to
  * even), in [-127, 127].  A row whose scale would be below 2^-126 is held as
- * scale 0 and steps 0; a row with an infinity or a NaN as scale NaN and steps
- * 0, so that every product with it is NaN.
+ * scale 0 and steps 0; a row with an infinity or a NaN, in y or in what it is
+ * formed from, as scale NaN and steps 0, so that every product with it is NaN.
  *
  * Ownership and errors as gdn_chunk_fwd: caller-allocated device buffers,
  * arguments checked on the host before any launch, asynchronous on `stream`.
  * Calls with no rows (or sequences) return GDN_OK and launch nothing.  Strides
  * are in elements.  None of the calls keeps state or allocates.  They may be
- * captured into CUDA graphs.  Small grids are launched so that they may begin
- * before the kernel ahead of them on the stream has ended (programmatic stream
- * serialization); they wait for its end before they read or write. */
+ * captured into CUDA graphs.  Most kernels (small grids, and of every size the
+ * single-token recurrence, the product and its copies) are launched so that they
+ * may begin before the kernel ahead of them on the stream has ended (programmatic
+ * stream serialization); they wait for its end before they read or write. */
 
 /* Gated delta rule, token by token, on a pool of states:
  *
@@ -423,7 +424,7 @@ typedef struct {
     int32_t pool;               /* states in the pool (>= 1) */
     int32_t io_dtype, o_dtype;  /* gdn_dtype of q, k, v; of o */
     int32_t qk_norm;            /* 0: q, k as given; 1: normalised here */
-    float qk_eps;               /* >= 0 */
+    float qk_eps;               /* > 0 with qk_norm, else not read */
     const void *q, *k, *v;      /* [rows][Hk][dk], [rows][Hk][dk], [rows][H][dv] */
     int64_t q_row, q_head, k_row, k_head, v_row, v_head;   /* strides (>= 0) */
     const float *alpha, *beta;  /* [rows][H] (heads adjacent), or NULL (=> 1) */
@@ -444,14 +445,16 @@ GDN_API gdn_status gdn_recurrent_fwd(const gdn_recurrent_args *args, void *strea
  *   GDN_ROWS_GATED  for each head of `head` channels: y = x / sqrt(mean(x^2) + eps)
  *                   * weight * gate / (1 + e^-gate); the scale is the whole row's
  *
- * Sums of squares are fp32.  residual_out may be residual itself, or x itself
+ * Sums of squares are fp32 and hold any finite numbers; h, h * weight and y past
+ * fp32 are infinities.  residual_out may be residual itself, or x itself
  * when the types and the strides agree; no other output may overlap an input. */
 typedef enum { GDN_ROWS_PLAIN = 0, GDN_ROWS_NORM = 1, GDN_ROWS_GATED = 2 } gdn_rows_op;
 
 typedef struct {
     int32_t op;                 /* gdn_rows_op */
     int32_t rows, width;        /* rows >= 0; 1 <= width <= 32768 */
-    int32_t head;               /* GATED: channels a head, a multiple of 8 up to 256 that divides width */
+    int32_t head;               /* GATED: channels a head, a multiple of 8 up to 256 that divides width;
+                                   heads times (head / 8 rounded up to a power of two) at most 4096 */
     int32_t x_dtype, residual_dtype, weight_dtype;   /* gdn_dtype; gate has x's */
     float eps;                  /* > 0 (NORM, GATED) */
     const void *x;              /* [rows][width] */
