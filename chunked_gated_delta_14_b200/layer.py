@@ -137,6 +137,11 @@ def _code(dt):
     return _DTYPES[dt]
 
 
+def _eps(x):
+    """x as the struct's 32 bits hold it."""
+    return ctypes.c_float(x).value
+
+
 def _ptr(t):
     return 0 if t is None else t.data_ptr()
 
@@ -265,7 +270,7 @@ def recurrent_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, alpha: Opti
         out = (torch.empty if cu_seqlens is None else torch.zeros)((N, H, dv), device=dev, dtype=od)
     row = lambda t: 0 if t is None else t.stride(0)  # noqa: E731
     _launch("gdn_recurrent_fwd", _pack_recurrent(
-        N, S, H, Hk, dk, dv, P, _DTYPES[io], code, 0 if qk_norm_eps is None else 1, qk_norm_eps or 0.0,
+        N, S, H, Hk, dk, dv, P, _DTYPES[io], code, 0 if qk_norm_eps is None else 1, 0.0 if qk_norm_eps is None else _eps(qk_norm_eps),
         _ptr(q), _ptr(k), _ptr(v), *q.stride()[:2], *k.stride()[:2], *v.stride()[:2], _ptr(alpha), _ptr(beta), row(alpha), row(beta),
         _ptr(cu_seqlens), _ptr(slots), _ptr(state), _ptr(out)), dev.index)
     return out
@@ -320,7 +325,7 @@ def add_rms_norm_int8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, re
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
     q, qr, scale = _steps(shape[:-1], D, dev)
-    _launch("gdn_rows_int8", _pack_rows(ROWS_NORM, rows, D, 0, _DTYPES[x.dtype], rdt, wdt, eps, _ptr(x), _ptr(residual), 0, wp, xr, rr, 0,
+    _launch("gdn_rows_int8", _pack_rows(ROWS_NORM, rows, D, 0, _DTYPES[x.dtype], rdt, wdt, _eps(eps), _ptr(x), _ptr(residual), 0, wp, xr, rr, 0,
                                         ror, qr, _ptr(residual_out), _ptr(q), _ptr(scale)), dev.index)
     return q, scale, residual_out
 
@@ -346,7 +351,8 @@ def gated_rms_norm_int8(x: torch.Tensor, gate: torch.Tensor, weight: Optional[to
 
     x, gate: [..., H, d] (bf16 or fp32, same dtype; the heads of a row adjacent, any row
     stride), d a multiple of 8 up to 256, H * d up to 32768 (H * (d / 8, rounded up to a power of
-    two) up to 4096); weight: [d] (bf16 or fp32; None = 1).  q: [..., H * d] int8, its rows on 16-byte boundaries; scale: [...] fp32, one for all heads of a row."""
+    two) up to 4096); weight: [d] (bf16 or fp32; None = 1).  q: [..., H * d] int8, its rows on
+    16-byte boundaries; scale: [...] fp32, one for all heads of a row."""
     if stream is not None:
         return _other_stream(stream, x, (x, gate, weight), lambda: gated_rms_norm_int8(x, gate, weight, eps=eps))
     r = (_quick or _bind_quick()).gated_rms_norm_int8(x, gate, weight, eps)
@@ -359,7 +365,7 @@ def gated_rms_norm_int8(x: torch.Tensor, gate: torch.Tensor, weight: Optional[to
     rows, xr = _head_rows(x, "x")
     gr = _head_rows(gate, "gate")[1]
     q, qr, scale = _steps(lead, H * d, dev)
-    _launch("gdn_rows_int8", _pack_rows(ROWS_GATED, rows, H * d, d, _DTYPES[x.dtype], 0, wdt, eps, _ptr(x), 0, _ptr(gate), wp, xr,
+    _launch("gdn_rows_int8", _pack_rows(ROWS_GATED, rows, H * d, d, _DTYPES[x.dtype], 0, wdt, _eps(eps), _ptr(x), 0, _ptr(gate), wp, xr,
                                         0, gr, 0, qr, 0, _ptr(q), _ptr(scale)), dev.index)
     return q, scale
 

@@ -4,6 +4,7 @@ overlapping rows, captures over two streams.
 
 Tolerances are those of test_layer_gpu.py, derived there beside each check.
 """
+import math
 
 import pytest
 import torch
@@ -382,4 +383,27 @@ def test_captured_over_two_streams():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want)) and torch.equal(s1, s0)
+    gdn.device_check()
+
+
+@pytest.mark.parametrize("quick", [True, False])
+def test_eps_of_other_types(quick, monkeypatch):
+    import chunked_gated_delta_14_b200.layer as L
+    if not quick:
+        monkeypatch.setattr(L, "_quick", L._NoQuick)
+    x = randn(rng(89), 4, 64)
+    q, state = x.view(4, 1, 64), torch.zeros(4, 1, 64, 64, device="cuda")
+    for f in (lambda e: gdn.add_rms_norm_int8(x, eps=e), lambda e: gdn.gated_rms_norm_int8(q, q, eps=e),
+              lambda e: gdn.recurrent_fwd(q, q, q, None, None, state, qk_norm_eps=e)):
+        for eps in ("1e-6", [1.0]):
+            with pytest.raises(TypeError):
+                f(eps)
+        for eps in (0, 0.0, -1, math.nan, 1e-60):
+            with pytest.raises(gdn.GDNError, match="eps"):
+                f(eps)
+        for eps in (1, True, 1e60, 10 ** 400):
+            try:
+                f(eps)
+            except OverflowError:
+                assert eps == 10 ** 400
     gdn.device_check()
